@@ -287,6 +287,140 @@ int tq_q8_logits(const void* packed, int d, int64_t n_seq, int n_kv, int64_t n_t
                  tq_dtype q_dtype, int g, const void* tail, int n_tail, float scale, float* out,
                  void* stream);
 
+/* Paged 8-bit cache ("b8"): keys and values at 8 bits with one scale for each block of 32
+ * tokens and head, appended to token by token, read by decode attention, by attention over
+ * selected blocks, and shortened by eviction. The engineering configuration list of
+ * blog.hotdry.top keeps recent tokens at full precision; here they are the tokens of the block
+ * that is not full yet.
+ *
+ * A page holds 32 tokens of all kv heads: keys, values, scales and key summaries. The table names
+ * the pages of each sequence; page j of a sequence holds its tokens 32 j .. 32 j + 31. The last
+ * len mod 32 tokens of a sequence wait in bf16 in its open block and move to a page, quantized
+ * once, when the block is full.
+ *   d          head size, 8..256, multiple of 8; D = 64, 128 or 256 is d rounded up.
+ *   n_kv       kv heads, 1..1024.
+ *   n_seq      sequences, 0..65535.
+ *   n_pages    pages in the pool, < 2^31.
+ *   max_blocks entries of a table row, 1..2^25: a sequence holds at most 32 max_blocks tokens.
+ *   pages      device, n_pages * tq_b8_page_bytes(d, n_kv) bytes, 128-byte aligned.
+ *   table      device int32 [n_seq, max_blocks], page numbers. Only the entries of full blocks are
+ *              read (and, by append, of the blocks it fills). Two sequences may share pages that
+ *              neither of them fills any more.
+ *   len        device int32 [n_seq], tokens of each sequence, the open ones included.
+ *   open       device bf16 [n_seq, n_kv, 2, 32, d]: the open block's keys, then its values, 16-byte
+ *              aligned.
+ * The arrays are the caller's; len and table are read when the work runs, so a captured graph
+ * follows them. A length outside 0 .. 32 max_blocks or a page outside the pool raises
+ * TQ_ERR_RANGE in the status word; such a sequence counts as empty, such a page is left out
+ * of sums and not written.
+ *
+ * Values. A token is rounded to bf16 when it comes in. With a = max |x| over the 32 x d values of a
+ * block, its scale is a / 127 and its codes are rint(x * inv), inv = 127 / a (a quotient in fp32,
+ * the product rounded once, halves to even). Values that are not finite count as 0 and raise
+ * TQ_ERR_RANGE when their block is quantized; for a < 2^-100 scale and codes are 0. So a cache does
+ * not depend on how its tokens were split over calls.
+ * Page layout. Header: n_kv entries of 32 + 2 D bytes: key scale, value scale (fp32), 24 bytes
+ * unused, lo[D], hi[D] (int8, smallest and largest key code of each channel over the 32 tokens);
+ * padded to a multiple of 128 bytes. Then n_kv entries of 64 D bytes: keys [32][D], values [32][D],
+ * each code a byte (code + 128). 16-byte chunk c of token t is chunk c ^ swz(t) of its row, with
+ * swz(t) = ((t & 2) | (((t ^ (t >> 2)) & 1) << 2)) & (D / 16 - 1). Channels d .. D-1 hold code 0. */
+#define TQ_B8_BLOCK 32
+typedef struct {
+    int d;
+    int n_kv;
+    int64_t n_seq;
+    int64_t n_pages;
+    int64_t max_blocks;
+    void* pages;
+    const int32_t* table;
+    const int32_t* len;
+    void* open;
+} tq_b8_cache;
+
+/* Bytes of one page; 0 if d or n_kv is unsupported. */
+size_t tq_b8_page_bytes(int d, int n_kv);
+
+/* Workspace of any tq_b8 call on this cache, 256-byte aligned, status word first. n_q, g: as in
+ * tq_b8_attention and tq_b8_select (0 if neither is called); n_sel: entries of a selection (0:
+ * none); weights: nonzero if tq_b8_attention is called with acc_out. 0 if unsupported. Calls
+ * whose work may overlap (other streams, graphs) need workspaces of their own.            */
+size_t tq_b8_workspace_bytes(const tq_b8_cache* cache, int n_q, int g, int n_sel, int weights);
+
+/* Appends tokens. len already counts them: token j of sequence s takes position
+ * len[s] - add[s] + j.
+ *   k, v      device, fp32 or bf16, 16-byte aligned: element (s, j, h, i) at s * seq_stride +
+ *             j * tok_stride + h * d + i, j < n_new; strides in elements, multiples of 8.
+ *   add       device int32 [n_seq], tokens that come to each sequence, 0 .. n_new (rows behind
+ *             them are not read), or NULL: n_new to each. add[s] > len[s] is a length out of range.
+ * Blocks that become full are written to their pages, tokens of the last one to the open block. */
+int tq_b8_append(const tq_b8_cache* cache, const void* k, const void* v, tq_dtype dtype, int64_t n_new,
+                 int64_t seq_stride, int64_t tok_stride, const int32_t* add, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/* Hands the last n_tok tokens of every sequence back as values: row j of sequence s is the token
+ * at position len[s] - n_tok + j. k, v: device, dtype [n_seq, n_tok, n_kv, d], 16-byte aligned.
+ * Rows before a sequence's first token, and of pages outside the pool, are left as they were. */
+int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dtype dtype, void* ws,
+               size_t ws_bytes, void* stream);
+
+/* Decode attention over the cache: for each of the n_q newest tokens of a sequence (at positions
+ * p = len - n_q + i, already appended) and each query head j, with kv head j / g,
+ *   out = sum_t w_t v_t,  w = softmax over t <= p of scale <q, k_t>.
+ * A query whose position is negative, or that sees no token, gives zeros.
+ *   q         device [n_seq, n_q, n_kv * g, d], fp32 or bf16; n_q, g >= 1, n_q * g <= 16384.
+ *   sel       device int32 [n_seq, n_q, n_kv, n_sel] block numbers from tq_b8_select: the query
+ *             sees only tokens of these blocks and of the open block; entries outside the
+ *             full blocks are passed over; an entry that is named twice counts twice. NULL with
+ *             n_sel = 0: all blocks.
+ *   acc_out   device fp32 [n_seq, n_kv, 32 * max_blocks] or NULL: receives decay * acc_in + the sum
+ *             of w_t over the g heads and n_q queries, for positions below len; others are left
+ *             as they were. acc_in (the same shape; may be acc_out itself; NULL: zeros) is read
+ *             at positions below len - n_q only: newer tokens start from zero. With sel,
+ *             n_q = 1 (else TQ_ERR_UNSUPPORTED) and no block may be named twice.
+ *   out       device fp32 [n_seq, n_q, n_kv * g, d], 16-byte aligned.
+ *   ws        tq_b8_workspace_bytes(cache, n_q, g, n_sel, acc_out != NULL) bytes.
+ * Logits are exact products of the codes with q held to 22 bits (bf16 q: exactly), weights
+ * carry 22 bits into the value sum; all sums are fp32. Runs give the same bits every time. */
+int tq_b8_attention(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int n_q, int g, float scale,
+                    const int32_t* sel, int n_sel, const float* acc_in, float* acc_out, float decay, float* out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* Chooses blocks for tq_b8_attention by a bound on their logits. A query head is held as
+ * qi = rint(q * (127 / max |q|)) (as codes are; a head with a value that is not finite, or with
+ * max |q| < 2^-100, as 0) and step = max |q| / 127; for a block with key scale s,
+ *   score = max over the g heads of (float(sum_i max(qi_i lo_i, qi_i hi_i)) * s) * step,
+ * two fp32 products. Candidates are the full blocks that begin at or before the query's position.
+ * The first n_first and the last n_last of them are always chosen, then those of the largest
+ * score, ties to the lowest number.
+ *   q, n_q, g as in tq_b8_attention; 0 <= n_first, n_last; n_first + n_last <= n_sel.
+ *   sel       device int32 [n_seq, n_q, n_kv, n_sel]: ascending, filled up with -1.
+ *   ws        tq_b8_workspace_bytes(cache, n_q, g, n_sel, 0) bytes.                       */
+int tq_b8_select(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int n_q, int g, int n_first, int n_last,
+                 int n_sel, int32_t* sel, void* ws, size_t ws_bytes, void* stream);
+
+/* Evicts tokens that were attended to least. Of the tokens in full blocks each kv head keeps
+ * 32 * keep_blocks (all of them if there are no more): the first n_first, the last n_last, then
+ * those of the largest acc (negative and NaN count as 0), ties to the lowest position; their order
+ * stays. They are written to new pages, quantized anew where tokens of several blocks meet: with
+ * each token's scale s_t and largest |code| c_t, a new block's scale is s' = max_t (c_t / 127) s_t
+ * and its codes are rint(code * (s_t / s')), quotients in fp32. A block that is kept whole keeps
+ * its bytes. The open block stays where it is.
+ *   acc       device fp32 [n_seq, n_kv, 32 * max_blocks], as tq_b8_attention leaves it.
+ *   keep_blocks  1 .. max_blocks, 32 * keep_blocks >= n_first + n_last.
+ *   dst_table device int32 [n_seq, max_blocks], the pages that receive the kept blocks (the first
+ *             keep_blocks entries are read). They must be other pages than those the table's
+ *             full blocks name, of any sequence, except that a sequence with no more than
+ *             keep_blocks full blocks may name its own pages in their order.
+ *   kept      device int32 [n_seq, n_kv, 32 * keep_blocks]: old positions, filled up with -1.
+ *   len_out   device int32 [n_seq], not len itself: the new lengths.
+ *   acc_out   device fp32 [n_seq, n_kv, 32 * max_blocks], not acc itself: acc of the tokens that
+ *             stay, at their new positions; positions behind the new length are left alone.
+ *   ws        tq_b8_workspace_bytes(cache, 0, 0, 0, 0) bytes.
+ * Afterwards dst_table and len_out with the same open block are the cache; the old pages are free. */
+int tq_b8_evict(const tq_b8_cache* cache, const float* acc, int64_t keep_blocks, int64_t n_first, int64_t n_last,
+                const int32_t* dst_table, int32_t* kept, int32_t* len_out, float* acc_out, void* ws, size_t ws_bytes,
+                void* stream);
+
 /* Diagnostic reconstruction (not on the hot path): x~ = |x|(Pi^T c[idx] + gamma
  * sqrt(pi/2)/m S^T s) for keys, |x| Pi^T c[idx] for values (blog.hotdry.top, "QJL residual
  * correction"). out: device fp32 [n_streams, n_tok, d].                                  */

@@ -31,7 +31,9 @@ EXPORTED = ["tq_make_codebook", "tq_block_bytes", "tq_record_bytes", "tq_packed_
             "tq_dequantize", "tq_reset_status", "tq_get_status", "tq_status_string", "tq_abi_version",
             "tq_logits_noalloc", "tq_attention", "tq_attention_workspace_bytes", "tq_logits_est", "tq_topk_est",
             "tq_q8_packed_bytes", "tq_q8_quantize", "tq_q8_logits", "tq_attention_q8",
-            "tq_attention_q8_workspace_bytes"]
+            "tq_attention_q8_workspace_bytes", "tq_b8_page_bytes", "tq_b8_workspace_bytes", "tq_b8_append",
+            "tq_b8_read", "tq_b8_attention", "tq_b8_select", "tq_b8_evict"]
+TQ_B8_BLOCK = 32
 
 
 class tq_codec(ctypes.Structure):
@@ -40,8 +42,15 @@ class tq_codec(ctypes.Structure):
                 ("prep", ctypes.c_void_p), ("prep_bytes", ctypes.c_size_t)]
 
 
+class tq_b8_cache(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int), ("n_kv", ctypes.c_int), ("n_seq", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64), ("pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("open", ctypes.c_void_p)]
+
+
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _CP = ctypes.POINTER(tq_codec)
+_BP = ctypes.POINTER(tq_b8_cache)
 _sig = {
     "tq_make_codebook": (_I, [_I, _I, _P, _P, _P]),
     "tq_block_bytes": (_SZ, [_CP]),
@@ -65,6 +74,13 @@ _sig = {
     "tq_q8_logits": (_I, [_P, _I, _I64, _I, _I64, _P, _I, _I, _P, _I, _F, _P, _P]),
     "tq_topk_est": (_I, [_CP, _P, _I64, _P, _I64, _I, _P, _P, _P, _SZ, _I, _P]),
     "tq_dequantize": (_I, [_CP, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "tq_b8_page_bytes": (_SZ, [_I, _I]),
+    "tq_b8_workspace_bytes": (_SZ, [_BP, _I, _I, _I, _I]),
+    "tq_b8_append": (_I, [_BP, _P, _P, _I, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+    "tq_b8_read": (_I, [_BP, _I64, _P, _P, _I, _P, _SZ, _P]),
+    "tq_b8_attention": (_I, [_BP, _P, _I, _I, _I, _F, _P, _I, _P, _P, _F, _P, _P, _SZ, _P]),
+    "tq_b8_select": (_I, [_BP, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "tq_b8_evict": (_I, [_BP, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "tq_reset_status": (_I, [_P, _P]),
     "tq_get_status": (_I, [_P, _P]),
     "tq_status_string": (ctypes.c_char_p, [_I]),
@@ -233,6 +249,143 @@ def tq_q8_quantize(x, d, n_streams, n_tok, x_stream_stride, packed, ws, stream=N
 def tq_q8_logits(packed, d, n_seq, n_kv, n_tok, q, g, tail, n_tail, scale, out, stream=None):
     return _check("tq_q8_logits", lib.tq_q8_logits(_ptr(packed), d, n_seq, n_kv, n_tok, _ptr(q), _dtype(q), g,
                                                    _ptr(tail), n_tail, scale, _ptr(out), _stream(stream)))
+
+
+def tq_b8_page_bytes(d, n_kv):
+    return lib.tq_b8_page_bytes(d, n_kv)
+
+
+class Cache8:
+    """A tq_b8_cache over the caller's tensors (kept alive here, all on one GPU).
+
+    pages uint8 [n_pages, tq_b8_page_bytes(d, n_kv)], table int32 [n_seq, max_blocks], length int32
+    [n_seq], open_ bf16 [n_seq, n_kv, 2, 32, d]. Their contents may change between calls."""
+
+    def __init__(self, d, pages, table, length, open_):
+        import torch
+        if open_.dim() != 5 or tuple(open_.shape[2:]) != (2, TQ_B8_BLOCK, d):
+            raise ValueError(f"open_ is [n_seq, n_kv, 2, {TQ_B8_BLOCK}, {d}]: got {tuple(open_.shape)}")
+        n_seq, n_kv = open_.shape[:2]
+        nbytes = lib.tq_b8_page_bytes(d, n_kv)
+        if nbytes == 0:
+            raise TQError("tq_b8_page_bytes", TQ_ERR_UNSUPPORTED)
+        self.d, self.n_kv, self.n_seq, self.device = d, n_kv, n_seq, pages.device
+        if pages.dim() != 2 or table.dim() != 2:
+            raise ValueError("pages is [n_pages, page bytes], table is [n_seq, max_blocks]")
+        self.max_blocks = table.shape[1]
+        _tensor(self, "pages", pages, torch.uint8, (pages.shape[0], nbytes))
+        _tensor(self, "table", table, torch.int32, (n_seq, table.shape[1]))
+        _tensor(self, "length", length, torch.int32, (n_seq,))
+        _tensor(self, "open_", open_, torch.bfloat16, (n_seq, n_kv, 2, TQ_B8_BLOCK, d))
+        self.pages, self.table, self.length, self.open_ = pages, table, length, open_
+        self.c = tq_b8_cache(d, n_kv, n_seq, pages.shape[0], table.shape[1], pages.data_ptr(), table.data_ptr(),
+                             length.data_ptr(), open_.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+def _tensor(cache, name, t, dtype, shape):
+    """t's address, after the checks that a wrong tensor would fail silently."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is wanted")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return t.data_ptr()
+
+
+def _b8_call(name, cache, ws, stream, *args):
+    """Enqueues lib.<name>(cache, *args, ws, stream) on the cache's GPU."""
+    import torch
+    if ws.device != cache.device:
+        raise ValueError(f"ws is on {ws.device}, the cache on {cache.device}")
+    dev = cache.device.index
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    here = torch._C._cuda_getDevice()
+    if here == dev:
+        return _check(name, getattr(lib, name)(cache.ref, *args, ws.data_ptr(), ws.numel(), handle))
+    with torch.cuda.device(dev):
+        return _check(name, getattr(lib, name)(cache.ref, *args, ws.data_ptr(), ws.numel(), handle))
+
+
+def _queries(cache, q):
+    if q.dim() != 4 or q.shape[2] % cache.n_kv:
+        raise ValueError(f"q is [n_seq, n_q, n_kv * g, d] with n_kv = {cache.n_kv}: got {tuple(q.shape)}")
+    n_q, g = q.shape[1], q.shape[2] // cache.n_kv
+    return _tensor(cache, "q", q, q.dtype, (cache.n_seq, n_q, cache.n_kv * g, cache.d)), _dtype(q), n_q, g
+
+
+def tq_b8_workspace_bytes(cache, n_q=0, g=0, n_sel=0, weights=True):
+    n = lib.tq_b8_workspace_bytes(cache.ref, n_q, g, n_sel, int(weights))
+    if n == 0:
+        raise TQError("tq_b8_workspace_bytes", TQ_ERR_UNSUPPORTED)
+    return n
+
+
+def tq_b8_append(cache, k, v, ws, add=None, stream=None):
+    """k, v [n_seq, n_new, n_kv, d] (views with other sequence and token strides too); cache.length counts them."""
+    import torch
+    shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d)
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 4 or tuple(t.shape) != shape or t.dtype != k.dtype:
+            raise ValueError(f"{name}: shape {shape} and {k.dtype} wanted, got {tuple(t.shape)} and {t.dtype}")
+        if t.device != cache.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+        st = t.stride()
+        if t.numel() and ((cache.d > 1 and st[3] != 1) or (cache.n_kv > 1 and st[2] != cache.d)):
+            raise ValueError(f"{name}: heads and channels lie next to each other, got strides {st}")
+    ks, vs = k.stride(), v.stride()
+    seq = [st[0] if cache.n_seq > 1 else 0 for st in (ks, vs)]
+    tok = [st[1] if shape[1] > 1 else 0 for st in (ks, vs)]
+    if seq[0] != seq[1] or tok[0] != tok[1]:
+        raise ValueError(f"k and v have other strides: {ks}, {vs}")
+    counts = None if add is None else _tensor(cache, "add", add, torch.int32, (cache.n_seq,))
+    return _b8_call("tq_b8_append", cache, ws, stream, k.data_ptr(), v.data_ptr(), _dtype(k), shape[1], seq[0], tok[0],
+                    counts)
+
+
+def tq_b8_read(cache, k, v, ws, stream=None):
+    """The last n_tok tokens of every sequence into k, v [n_seq, n_tok, n_kv, d] (fp32 or bf16)."""
+    shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d)
+    kp, vp = _tensor(cache, "k", k, k.dtype, shape), _tensor(cache, "v", v, k.dtype, shape)
+    return _b8_call("tq_b8_read", cache, ws, stream, shape[1], kp, vp, _dtype(k))
+
+
+def tq_b8_attention(cache, q, scale, out, ws, sel=None, acc_in=None, acc_out=None, decay=1.0, stream=None):
+    import torch
+    qp, dt, n_q, g = _queries(cache, q)
+    op = _tensor(cache, "out", out, torch.float32, q.shape)
+    sp, n_sel = None, 0
+    if sel is not None:
+        n_sel = sel.shape[-1]
+        sp = _tensor(cache, "sel", sel, torch.int32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+    row = (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * cache.max_blocks)
+    ip = None if acc_in is None else _tensor(cache, "acc_in", acc_in, torch.float32, row)
+    ap = None if acc_out is None else _tensor(cache, "acc_out", acc_out, torch.float32, row)
+    return _b8_call("tq_b8_attention", cache, ws, stream, qp, dt, n_q, g, scale, sp, n_sel, ip, ap, decay, op)
+
+
+def tq_b8_select(cache, q, sel, ws, n_first=1, n_last=1, stream=None):
+    """Fills sel int32 [n_seq, n_q, n_kv, n_sel] with the blocks tq_b8_attention is to look at."""
+    import torch
+    qp, dt, n_q, g = _queries(cache, q)
+    n_sel = sel.shape[-1]
+    sp = _tensor(cache, "sel", sel, torch.int32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+    return _b8_call("tq_b8_select", cache, ws, stream, qp, dt, n_q, g, n_first, n_last, n_sel, sp)
+
+
+def tq_b8_evict(cache, acc, keep_blocks, dst_table, kept, length_out, acc_out, ws, n_first=0, n_last=0, stream=None):
+    import torch
+    row = (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * cache.max_blocks)
+    ap, op = _tensor(cache, "acc", acc, torch.float32, row), _tensor(cache, "acc_out", acc_out, torch.float32, row)
+    dp = _tensor(cache, "dst_table", dst_table, torch.int32, (cache.n_seq, cache.max_blocks))
+    kp = _tensor(cache, "kept", kept, torch.int32, (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * keep_blocks))
+    lp = _tensor(cache, "length_out", length_out, torch.int32, (cache.n_seq,))
+    return _b8_call("tq_b8_evict", cache, ws, stream, ap, keep_blocks, n_first, n_last, dp, kp, lp, op)
 
 
 def tq_dequantize(codec: Codec, packed, n_streams, n_tok, out, ws=None, stream=None):

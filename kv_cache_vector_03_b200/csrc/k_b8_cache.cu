@@ -1,0 +1,234 @@
+// Paged 8-bit cache: tokens in (tq_b8_append), tokens back out (tq_b8_read).
+//
+// Append. One warp per (sequence, head, keys or values, block that the call touches). A lane holds
+// 8 channels of D/8 tokens in registers, so a block is read once: its largest |x| (an integer
+// maximum over the bf16 bits, which also shows values that are not finite) gives the scale, then
+// every value becomes a code by one fused multiply-add with 1.5 * 2^23 + 128: the sum's rounding is
+// the rounding of the exact product to a whole number, halves to even, and its low byte is
+// code + 128. The smallest and largest code of a channel are the codes of its smallest and largest
+// value, since the map is monotone. The warp of a call's first block reads the open block's
+// tokens and then, in program order, writes the tokens that stay open, so no other warp
+// touches the open block.
+#include "k_b8.cuh"
+
+namespace {
+
+constexpr float kRound = 12583040.f;     // 1.5 * 2^23 + 128
+constexpr int kAppendWarps = 4;
+constexpr int kReadWarps = 8;
+
+// 8 channels as bf16 pairs
+template <bool F32>
+TQ_DEVICE uint4 load8(const void* base, int64_t elem) {
+    if (!F32) return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
+    const float4 a = f[0], b = f[1];
+    const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
+                                 __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
+    return *reinterpret_cast<const uint4*>(r);
+}
+
+TQ_DEVICE uint32_t code2(uint32_t w, float inv) {   // two codes + 128 in the low two bytes
+    const float lo = fmaf(__uint_as_float(w << 16), inv, kRound);
+    const float hi = fmaf(__uint_as_float(w & 0xffff0000u), inv, kRound);
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
+}
+TQ_DEVICE uint2 code8(uint4 x, float inv) {
+    return make_uint2(__byte_perm(code2(x.x, inv), code2(x.y, inv), 0x5410),
+                      __byte_perm(code2(x.z, inv), code2(x.w, inv), 0x5410));
+}
+TQ_DEVICE uint32_t drop_nonfinite(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+TQ_DEVICE uint32_t bf2_min(uint32_t a, uint32_t b) {
+    __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+TQ_DEVICE uint32_t bf2_max(uint32_t a, uint32_t b) {
+    __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_constant__ B8AppendParams p, int nbt) {
+    constexpr int CH = D / 8;        // 8-channel chunks of a row; also token steps of a lane
+    constexpr int TPI = 32 / CH;     // tokens of one step
+    const B8Cache& c = p.c;
+    const int lane = threadIdx.x & 31;
+    int64_t id = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int h = (int)(id % c.n_kv);
+    id /= c.n_kv;
+    const int side = (int)(id & 1);
+    id >>= 1;
+    const int j = (int)(id % nbt);
+    const int64_t s = id / nbt;
+    if (s >= c.n_seq) return;
+    const int n = b8_len(c, s);
+    const int64_t add = p.add ? p.add[s] : p.n_new;
+    if (add < 0 || add > p.n_new || add > n) {
+        if (lane == 0) tq_raise(c.status, TQ_FLAG_RANGE);
+        return;
+    }
+    if (add == 0) return;
+    const int first = n - (int)add, b0 = first >> 5, b1 = n >> 5, b = b0 + j;
+    const void* src = side ? p.v : p.k;
+    uint16_t* open = b8_open(c, s, h, side);
+    const int64_t row0 = s * p.seq_stride + (int64_t)h * c.d;
+    const int ch = lane % CH, t0 = lane / CH;
+    const bool in = ch * 8 < c.d;
+    if (b < b1) {
+        uint8_t* page = b8_page(c, c.table[s * c.max_blocks + b]);
+        uint4 x[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int t = t0 + i * TPI, pos = 32 * b + t;
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (in)
+                x[i] = pos < first ? *reinterpret_cast<const uint4*>(open + t * c.d + ch * 8)
+                                   : load8<F32>(src, row0 + (pos - first) * p.tok_stride + ch * 8);
+        }
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            m = __vmaxu2(__vmaxu2(m, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)),
+                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        if (m >= 0x7f80u) {
+            if (lane == 0) tq_raise(c.status, TQ_FLAG_RANGE);
+            m = 0u;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                x[i] = make_uint4(drop_nonfinite(x[i].x), drop_nonfinite(x[i].y), drop_nonfinite(x[i].z),
+                                  drop_nonfinite(x[i].w));
+                m = __vmaxu2(__vmaxu2(m, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)),
+                             __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+            }
+            m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        }
+        const float a = __uint_as_float(m << 16);
+        const bool live = a >= kB8MinMax;
+        const float inv = live ? 127.f / a : 0.f, scale = live ? a / 127.f : 0.f;
+        if (page) {
+            uint8_t* rows = b8_codes(c, page, h, side);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int t = t0 + i * TPI;
+                *reinterpret_cast<uint2*>(rows + t * D + (((ch >> 1) ^ b8_swz(t, D / 16)) << 4) + (ch & 1) * 8) =
+                    code8(x[i], inv);
+            }
+            uint8_t* e = b8_entry(c, page, h);
+            if (lane == 0) *reinterpret_cast<float*>(e + 4 * side) = scale;
+            if (side == 0) {
+                uint4 lo = x[0], hi = x[0];
+#pragma unroll
+                for (int i = 1; i < CH; ++i) {
+                    lo = make_uint4(bf2_min(lo.x, x[i].x), bf2_min(lo.y, x[i].y), bf2_min(lo.z, x[i].z),
+                                    bf2_min(lo.w, x[i].w));
+                    hi = make_uint4(bf2_max(hi.x, x[i].x), bf2_max(hi.y, x[i].y), bf2_max(hi.z, x[i].z),
+                                    bf2_max(hi.w, x[i].w));
+                }
+#pragma unroll
+                for (int o = CH; o < 32; o <<= 1) {
+                    lo = make_uint4(bf2_min(lo.x, __shfl_xor_sync(0xffffffffu, lo.x, o)),
+                                    bf2_min(lo.y, __shfl_xor_sync(0xffffffffu, lo.y, o)),
+                                    bf2_min(lo.z, __shfl_xor_sync(0xffffffffu, lo.z, o)),
+                                    bf2_min(lo.w, __shfl_xor_sync(0xffffffffu, lo.w, o)));
+                    hi = make_uint4(bf2_max(hi.x, __shfl_xor_sync(0xffffffffu, hi.x, o)),
+                                    bf2_max(hi.y, __shfl_xor_sync(0xffffffffu, hi.y, o)),
+                                    bf2_max(hi.z, __shfl_xor_sync(0xffffffffu, hi.z, o)),
+                                    bf2_max(hi.w, __shfl_xor_sync(0xffffffffu, hi.w, o)));
+                }
+                if (lane < CH) {
+                    uint2 l8 = code8(lo, inv), h8 = code8(hi, inv);
+                    *reinterpret_cast<uint2*>(e + 32 + ch * 8) = make_uint2(l8.x ^ 0x80808080u, l8.y ^ 0x80808080u);
+                    *reinterpret_cast<uint2*>(e + 32 + D + ch * 8) = make_uint2(h8.x ^ 0x80808080u, h8.y ^ 0x80808080u);
+                }
+            }
+        }
+    }
+    if (j == 0 && (n & 31)) {
+        __syncwarp();   // every lane has read what the open block held
+        if (in)
+            for (int pos = max(first, 32 * b1) + t0; pos < n; pos += TPI)
+                *reinterpret_cast<uint4*>(open + (pos & 31) * c.d + ch * 8) =
+                    load8<F32>(src, row0 + (pos - first) * p.tok_stride + ch * 8);
+    }
+}
+
+// one warp per (sequence, token, keys or values); a lane takes 8 channels of a head at a time
+template <int D, bool F32>
+__global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p) {
+    const B8Cache& c = p.c;
+    const int lane = threadIdx.x & 31;
+    int64_t id = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+    const int side = (int)(id & 1);
+    id >>= 1;
+    const int64_t s = id / p.n_tok, j = id - s * p.n_tok;
+    if (s >= c.n_seq) return;
+    const int n = b8_len(c, s);
+    const int64_t pos = n - p.n_tok + j;
+    if (pos < 0) return;
+    const int b = (int)(pos >> 5), t = (int)(pos & 31), chunks = c.d / 8;
+    const bool paged = b < (n >> 5);
+    uint8_t* page = nullptr;
+    if (paged && !(page = b8_page(c, c.table[s * c.max_blocks + b]))) return;
+    const int64_t row = (s * p.n_tok + j) * c.n_kv * c.d;
+    for (int i = lane; i < c.n_kv * chunks; i += 32) {
+        const int h = i / chunks, ch = i - h * chunks;
+        float f[8];
+        if (paged) {
+            const float sc = *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side);
+            const uint2 w = *reinterpret_cast<const uint2*>(b8_codes(c, page, h, side) + t * D +
+                                                            (((ch >> 1) ^ b8_swz(t, D / 16)) << 4) + (ch & 1) * 8);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                f[k] = sc * (float)((int)(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 0xffu) - 128);
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(b8_open(c, s, h, side) + t * c.d + ch * 8);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(k & 1 ? u[k >> 1] & 0xffff0000u : u[k >> 1] << 16);
+        }
+        const int64_t at = row + (int64_t)h * c.d + ch * 8;
+        if (F32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(side ? p.v : p.k) + at);
+            o[0] = make_float4(f[0], f[1], f[2], f[3]);
+            o[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            __nv_bfloat162 r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(side ? p.v : p.k) + at) = *reinterpret_cast<uint4*>(r);
+        }
+    }
+}
+
+}  // namespace
+
+#define B8_DISPATCH(KERN, ...)                                                                     \
+    do {                                                                                           \
+        if (p.c.D == 64) {                                                                         \
+            if (p.dtype) KERN<64, false><<<__VA_ARGS__; else KERN<64, true><<<__VA_ARGS__;         \
+        } else if (p.c.D == 128) {                                                                 \
+            if (p.dtype) KERN<128, false><<<__VA_ARGS__; else KERN<128, true><<<__VA_ARGS__;       \
+        } else {                                                                                   \
+            if (p.dtype) KERN<256, false><<<__VA_ARGS__; else KERN<256, true><<<__VA_ARGS__;       \
+        }                                                                                          \
+    } while (0)
+
+cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st) {
+    const int64_t nbt = (p.n_new + 62) / 32;   // a call touches at most this many blocks of a sequence
+    const int64_t grid = (p.c.n_seq * nbt * 2 * p.c.n_kv + kAppendWarps - 1) / kAppendWarps;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    B8_DISPATCH(k_b8_append, (unsigned)grid, kAppendWarps * 32, 0, st>>>(p, (int)nbt));
+    return cudaGetLastError();
+}
+
+cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st) {
+    const int64_t grid = (p.c.n_seq * p.n_tok * 2 + kReadWarps - 1) / kReadWarps;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    B8_DISPATCH(k_b8_read, (unsigned)grid, kReadWarps * 32, 0, st>>>(p));
+    return cudaGetLastError();
+}

@@ -1,0 +1,367 @@
+// Choosing: blocks by a bound on their logits (tq_b8_select), tokens by accumulated attention
+// weight, and the move of the tokens that stay (tq_b8_evict).
+//
+// Score. For codes between lo_i and hi_i, sum_i qi_i code_i <= sum_i max(qi_i lo_i, qi_i hi_i) =
+// <min(qi, 0), lo> + <max(qi, 0), hi>: one int8 product of length 2 D with the block's summary,
+// exact in int32, on the int8 tensor cores (16 blocks x 8 heads per warp). A block costs 2 D + 4
+// bytes here where attention reads 64 D.
+//
+// Choice of the k largest of n. Keys are order-preserving 32-bit patterns. The k-th largest is
+// found digit by digit (11 + 11 + 10 bits) from histograms in shared memory; a last pass in
+// index order writes what lies above it and the first of what equals it, by prefix sums, so the
+// result is ascending and ties go to the lowest index.
+#include <cfloat>
+
+#include "k_b8.cuh"
+
+namespace {
+
+constexpr int kScoreWarps = 8;
+constexpr int kPickThreads = 512;
+constexpr int kMoveWarps = 4;
+constexpr float kRound = 12583040.f;     // 1.5 * 2^23 + 128: a sum's low byte is code + 128
+
+TQ_DEVICE uint32_t order_bits(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// full blocks that begin at or before the position of query token i
+TQ_DEVICE int candidates(int n, int n_q, int i) {
+    const int last = n - n_q + i;
+    return last < 0 ? 0 : min(n >> 5, (last >> 5) + 1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int tiles) {
+    constexpr int CH = D / 32;       // 16-byte chunks a lane takes of a summary's 2 D bytes
+    const B8Cache& c = p.c;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    int64_t rowid = blockIdx.x / tiles;
+    const int tile = (int)(blockIdx.x - rowid * tiles);
+    const int64_t out0 = rowid * c.max_blocks;
+    const int h = (int)(rowid % c.n_kv);
+    rowid /= c.n_kv;
+    const int i = (int)(rowid % p.n_q);
+    const int64_t s = rowid / p.n_q;
+    const int nb = candidates(b8_len(c, s), p.n_q, i);
+    const int b0 = (tile * kScoreWarps + w) * 16;
+    if (tile * kScoreWarps * 16 >= nb) return;
+    __shared__ uint32_t s_q[8][2 * D / 4 + 4];   // + 4 words: the 8 rows of a load fall on distinct banks
+    __shared__ float s_step[8];
+    // the summaries of this warp's 16 blocks: rows gq and gq + 8
+    uint4 a[2][CH];
+    float ks[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int b = b0 + gq + 8 * r;
+        const uint8_t* e = nullptr;
+        if (b < nb) {
+            uint8_t* page = b8_page(c, c.table[s * c.max_blocks + b]);
+            if (page) e = b8_entry(c, page, h);
+        }
+        ks[r] = e ? *reinterpret_cast<const float*>(e) : 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+            a[r][k] = e ? *reinterpret_cast<const uint4*>(e + 32 + 16 * (tq + 4 * k)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int g0 = 0; g0 < p.g; g0 += 8) {
+        if (g0) __syncthreads();
+        {   // warp w holds query head g0 + w as int8: negative parts against lo, positive ones against hi
+            const int j = g0 + w;
+            const int64_t at = (((s * p.n_q + i) * c.n_kv + h) * p.g + j) * c.d;
+            float v[D / 32], am = 0.f;
+            bool fin = true;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const int e = lane * (D / 32) + k;
+                v[k] = j < p.g && e < c.d ? tq_load_elem(p.q, p.q_dtype, at + e) : 0.f;
+                fin = fin && isfinite(v[k]);
+                am = fmaxf(am, fabsf(v[k]));
+            }
+            am = tq_warp_max(am);
+            const bool live = __all_sync(0xffffffffu, fin) && am >= kB8MinMax;
+            const float inv = live ? 127.f / am : 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const int e = lane * (D / 32) + k;
+                const int qi = live ? (int)(__float_as_uint(fmaf(v[k], inv, kRound)) & 0xffu) - 128 : 0;
+                reinterpret_cast<int8_t*>(s_q[w])[e] = (int8_t)min(qi, 0);
+                reinterpret_cast<int8_t*>(s_q[w])[D + e] = (int8_t)max(qi, 0);
+            }
+            if (lane == 0) s_step[w] = live ? am / 127.f : 0.f;
+        }
+        __syncthreads();
+        int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const uint32_t* b = &s_q[gq][4 * (tq + 4 * k)];
+            tq_imma(acc, a[0][k].x, a[1][k].x, a[0][k].y, a[1][k].y, b[0], b[1]);
+            tq_imma(acc, a[0][k].z, a[1][k].z, a[0][k].w, a[1][k].w, b[2], b[3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // blocks gq, gq, gq + 8, gq + 8; heads 2 tq, 2 tq + 1
+            const int j = 2 * tq + (k & 1);
+            if (g0 + j < p.g)
+                best[k >> 1] = fmaxf(best[k >> 1], __fmul_rn(__fmul_rn((float)acc[k], ks[k >> 1]), s_step[j]));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+        const int b = b0 + gq + 8 * r;
+        if (tq == 0 && b < nb) p.key[out0 + b] = order_bits(best[r]);
+    }
+}
+
+// ascending indices of the chosen of n: all of them if n <= k, else the first nf, the last nl and
+// the k - nf - nl largest keys between, ties to the lowest; the rest of out[0 .. k) is -1
+template <typename Key>
+TQ_DEVICE void pick(int64_t n, int64_t k, int64_t nf, int64_t nl, Key key, int32_t* out) {
+    __shared__ uint32_t s_hist[2048], s_cnt[2][kPickThreads / 32], s_digit, s_left;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    if (n <= k) {
+        for (int64_t j = tid; j < k; j += kPickThreads) out[j] = j < n ? (int32_t)j : -1;
+        return;
+    }
+    const int64_t m0 = nf, m1 = n - nl;
+    uint32_t left = (uint32_t)(k - nf - nl);      // how many the middle gives
+    uint32_t prefix = 0, mask = 0;
+    const bool any = left > 0;
+    if (any) {
+        for (int pass = 0; pass < 3; ++pass) {
+            const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            for (int b = tid; b < 2048; b += kPickThreads) s_hist[b] = 0;
+            __syncthreads();
+            for (int64_t t = m0 + tid; t < m1; t += kPickThreads) {
+                const uint32_t u = key(t);
+                if ((u & mask) == prefix) atomicAdd(&s_hist[(u >> sh) & ((1u << bits) - 1)], 1u);
+            }
+            __syncthreads();
+            // the largest digit with at least `left` keys at or above it: one warp, from the top
+            if (w == 0) {
+                uint32_t above = 0;
+                for (int b = 2048 - 32; b >= 0; b -= 32) {
+                    const uint32_t v = s_hist[b + 31 - lane];      // lane 0 holds the highest bin
+                    uint32_t sum = v;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+                        if (lane >= o) sum += x;
+                    }
+                    const uint32_t hit = __ballot_sync(0xffffffffu, above + sum >= left);
+                    if (hit) {
+                        const int f = __ffs(hit) - 1;
+                        const uint32_t before = above + __shfl_sync(0xffffffffu, sum - v, f);
+                        if (lane == 0) {
+                            s_digit = b + 31 - f;
+                            s_left = left - before;
+                        }
+                        break;
+                    }
+                    above += __shfl_sync(0xffffffffu, sum, 31);
+                }
+            }
+            __syncthreads();
+            prefix |= s_digit << sh;
+            mask |= ((1u << bits) - 1) << sh;
+            left = s_left;
+            __syncthreads();
+        }
+    }
+    // `left` keys equal to prefix are still wanted, the lowest indices first
+    int64_t done = 0;
+    uint32_t ties = 0;
+    for (int64_t t0 = 0; t0 < n; t0 += kPickThreads) {
+        const int64_t t = t0 + tid;
+        bool take = t < n && (t < nf || t >= m1), tie = false;
+        if (any && t >= m0 && t < m1) {
+            const uint32_t u = key(t);
+            take = u > prefix;
+            tie = u == prefix;
+        }
+        const uint32_t below = (1u << lane) - 1;
+        const uint32_t bt = __ballot_sync(0xffffffffu, tie);
+        if (lane == 0) s_cnt[0][w] = __popc(bt);
+        __syncthreads();
+        uint32_t rank = ties, all = ties;
+        for (int v = 0; v < kPickThreads / 32; ++v) {
+            if (v < w) rank += s_cnt[0][v];
+            all += s_cnt[0][v];
+        }
+        rank += __popc(bt & below);
+        take = take || (tie && rank < left);
+        ties = all;
+        const uint32_t bk = __ballot_sync(0xffffffffu, take);
+        if (lane == 0) s_cnt[1][w] = __popc(bk);
+        __syncthreads();
+        int64_t at = done;
+        for (int v = 0; v < kPickThreads / 32; ++v) {
+            if (v < w) at += s_cnt[1][v];
+            done += s_cnt[1][v];
+        }
+        if (take) out[at + __popc(bk & below)] = (int32_t)t;
+    }
+}
+
+struct ScoreKey {
+    const uint32_t* key;
+    TQ_DEVICE uint32_t operator()(int64_t t) const { return key[t]; }
+};
+struct WeightKey {
+    const float* acc;
+    TQ_DEVICE uint32_t operator()(int64_t t) const { return __float_as_uint(fmaxf(acc[t], 0.f) + 0.f); }
+};
+
+__global__ void __launch_bounds__(kPickThreads) k_b8_pick_blocks(const __grid_constant__ B8SelectParams p) {
+    const int64_t row = blockIdx.x, si = row / p.c.n_kv, s = si / p.n_q;
+    const int nb = candidates(b8_len(p.c, s), p.n_q, (int)(si - s * p.n_q));
+    pick(nb, p.n_sel, p.n_first, p.n_last, ScoreKey{p.key + row * p.c.max_blocks}, p.sel + row * p.n_sel);
+}
+
+__global__ void __launch_bounds__(kPickThreads) k_b8_pick_tokens(const __grid_constant__ B8EvictParams p) {
+    const int64_t row = blockIdx.x, s = row / p.c.n_kv;
+    const int n = b8_len(p.c, s) & ~31;
+    pick(n, 32 * p.keep_blocks, p.n_first, p.n_last, WeightKey{p.acc + row * p.c.max_blocks * 32},
+         p.kept + row * 32 * p.keep_blocks);
+}
+
+// One warp per (sequence, new block, keys or values, head): gathers 32 kept tokens, finds the new
+// scale, requantizes by one multiply-add per code and writes the block, its scale and summary.
+// The warps of new block keep_blocks move what belongs to the open block: its acc, the length.
+template <int D>
+__global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_constant__ B8EvictParams p) {
+    constexpr int CH = D / 16, TPI = 32 / CH, IT = CH;   // 16-byte chunks of a row; tokens per step; steps
+    const B8Cache& c = p.c;
+    const int lane = threadIdx.x & 31;
+    int64_t id = (int64_t)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+    const int h = (int)(id % c.n_kv);
+    id /= c.n_kv;
+    const int side = (int)(id & 1);
+    id >>= 1;
+    const int64_t j = id % (p.keep_blocks + 1), s = id / (p.keep_blocks + 1);
+    if (s >= c.n_seq) return;
+    const int n = b8_len(c, s), nfull = n >> 5, r = n & 31;
+    const int left = (int)min((int64_t)nfull, p.keep_blocks);
+    const int64_t arow = (s * c.n_kv + h) * c.max_blocks * 32;
+    if (j == p.keep_blocks) {
+        if (side == 0 && lane < r) p.acc_out[arow + 32 * left + lane] = p.acc[arow + 32 * nfull + lane];
+        if (side == 0 && h == 0 && lane == 0) p.len_out[s] = 32 * left + r;
+        return;
+    }
+    if (j >= left) return;
+    const int tok = p.kept[((s * c.n_kv + h) * p.keep_blocks + j) * 32 + lane];
+    if (side == 0) p.acc_out[arow + 32 * j + lane] = p.acc[arow + tok];
+    uint8_t* page = b8_page(c, c.table[s * c.max_blocks + (tok >> 5)]);
+    uint8_t* dst = b8_page(c, p.dst_table[s * c.max_blocks + j]);
+    const float sc = page ? *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side) : 0.f;
+    const uint8_t* row = page ? b8_codes(c, page, h, side) + (tok & 31) * D : nullptr;
+    const int ch = lane % CH, t0 = lane / CH;
+    uint4 x[IT];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int t = t0 + i * TPI;
+        const uint8_t* rp = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)row, t));
+        const int tk = __shfl_sync(0xffffffffu, tok, t) & 31;
+        x[i] = rp ? *reinterpret_cast<const uint4*>(rp + ((ch ^ b8_swz(tk, CH)) << 4))
+                  : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            m = fmaxf(m, fabsf(__uint_as_float(__byte_perm(u[k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f));
+#pragma unroll
+        for (int o = 1; o < CH; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        top = fmaxf(top, __fmul_rn(m / 127.f, __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
+    }
+    top = tq_warp_max(top);
+    if (!dst) return;
+    const float ratio = top > 0.f ? sc / top : 0.f;
+    uint8_t* drow = b8_codes(c, dst, h, side);
+    float lo[16], hi[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        lo[k] = INFINITY;
+        hi[k] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int t = t0 + i * TPI;
+        const float rt = __shfl_sync(0xffffffffu, ratio, t);
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float cd = __uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f;
+                f[k] = fmaf(cd, rt, kRound);
+                lo[4 * q + k] = fminf(lo[4 * q + k], f[k]);
+                hi[4 * q + k] = fmaxf(hi[4 * q + k], f[k]);
+            }
+            o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
+                               __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
+        }
+        *reinterpret_cast<uint4*>(drow + t * D + ((ch ^ b8_swz(t, CH)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    uint8_t* e = b8_entry(c, dst, h);
+    if (lane == 0) *reinterpret_cast<float*>(e + 4 * side) = top;
+    if (side) return;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+        for (int o = CH; o < 32; o <<= 1) {
+            lo[k] = fminf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+            hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+        }
+    if (lane < CH) {
+        uint32_t l[4], g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            l[q] = g[q] = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                l[q] |= ((__float_as_uint(lo[4 * q + k]) ^ 0x80u) & 0xffu) << (8 * k);
+                g[q] |= ((__float_as_uint(hi[4 * q + k]) ^ 0x80u) & 0xffu) << (8 * k);
+            }
+        }
+        *reinterpret_cast<uint4*>(e + 32 + 16 * ch) = make_uint4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<uint4*>(e + 32 + D + 16 * ch) = make_uint4(g[0], g[1], g[2], g[3]);
+    }
+}
+
+}  // namespace
+
+cudaError_t b8_launch_select(const B8SelectParams& p, cudaStream_t st) {
+    const int64_t rows = p.c.n_seq * p.n_q * p.c.n_kv;
+    const int64_t tiles = (p.c.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
+    if (rows * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(rows * tiles);
+    if (p.c.D == 64) k_b8_score<64><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
+    else if (p.c.D == 128) k_b8_score<128><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
+    else k_b8_score<256><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    k_b8_pick_blocks<<<(unsigned)rows, kPickThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t b8_launch_evict(const B8EvictParams& p, cudaStream_t st) {
+    const int64_t rows = p.c.n_seq * p.c.n_kv;
+    const int64_t grid = (rows * 2 * (p.keep_blocks + 1) + kMoveWarps - 1) / kMoveWarps;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    k_b8_pick_tokens<<<(unsigned)rows, kPickThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (p.c.D == 64) k_b8_move<64><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
+    else if (p.c.D == 128) k_b8_move<128><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
+    else k_b8_move<256><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
+    return cudaGetLastError();
+}

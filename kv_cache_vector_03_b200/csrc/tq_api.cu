@@ -203,7 +203,7 @@ const char* tq_status_string(int s) {
         case TQ_ERR_ARG: return "invalid argument";
         case TQ_ERR_UNSUPPORTED: return "unsupported shape";
         case TQ_ERR_CUDA: return "CUDA runtime error";
-        case TQ_ERR_RANGE: return "norm overflowed binary16 or input not finite";
+        case TQ_ERR_RANGE: return "norm overflowed binary16, input not finite, or a cache length or page out of range";
         case TQ_ERR_TIMEOUT: return "timeout";
         case TQ_ERR_NOCONV: return "codebook did not converge";
         case TQ_ERR_WORKSPACE: return "workspace or prepared buffer too small";
