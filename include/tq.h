@@ -315,8 +315,9 @@ int tq_q8_logits(const void* packed, int d, int64_t n_seq, int n_kv, int64_t n_t
  * of sums and not written.
  *
  * Values. A token is rounded to bf16 when it comes in. With a = max |x| over the 32 x d values of a
- * block, its scale is a / 127 and its codes are rint(x * inv), inv = 127 / a (a quotient in fp32,
- * the product rounded once, halves to even). Values that are not finite count as 0 and raise
+ * block, its scale is a * (1 / 127) and its codes are rint(x * inv), inv = (1 / a) * 127 (each
+ * quotient and product rounded to fp32, but x * inv only once, to a whole number, halves to even).
+ * Values that are not finite count as 0 and raise
  * TQ_ERR_RANGE when their block is quantized; for a < 2^-100 scale and codes are 0. So a cache does
  * not depend on how its tokens were split over calls.
  * Page layout. Header: n_kv entries of 32 + 2 D bytes: key scale, value scale (fp32), 24 bytes
@@ -386,8 +387,8 @@ int tq_b8_attention(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, i
                     void* ws, size_t ws_bytes, void* stream);
 
 /* Chooses blocks for tq_b8_attention by a bound on their logits. A query head is held as
- * qi = rint(q * (127 / max |q|)) (as codes are; a head with a value that is not finite, or with
- * max |q| < 2^-100, as 0) and step = max |q| / 127; for a block with key scale s,
+ * qi = rint(q * inv), inv = (1 / max |q|) * 127 (as codes are; a head with a value that is not
+ * finite, or with max |q| < 2^-100, as 0) and step = max |q| * (1 / 127); for a block with key scale s,
  *   score = max over the g heads of (float(sum_i max(qi_i lo_i, qi_i hi_i)) * s) * step,
  * two fp32 products. Candidates are the full blocks that begin at or before the query's position.
  * The first n_first and the last n_last of them are always chosen, then those of the largest
@@ -402,8 +403,8 @@ int tq_b8_select(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int 
  * 32 * keep_blocks (all of them if there are no more): the first n_first, the last n_last, then
  * those of the largest acc (negative and NaN count as 0), ties to the lowest position; their order
  * stays. They are written to new pages, quantized anew where tokens of several blocks meet: with
- * each token's scale s_t and largest |code| c_t, a new block's scale is s' = max_t (c_t / 127) s_t
- * and its codes are rint(code * (s_t / s')), quotients in fp32. A block that is kept whole keeps
+ * each token's scale s_t and largest |code| c_t, a new block's scale is s' = max_t (c_t * (1 / 127)) s_t
+ * and its codes are rint(code * (s_t / s')), scales and quotients in fp32. A block that is kept whole keeps
  * its bytes. The open block stays where it is.
  *   acc       device fp32 [n_seq, n_kv, 32 * max_blocks], as tq_b8_attention leaves it.
  *   keep_blocks  1 .. max_blocks, 32 * keep_blocks >= n_first + n_last.

@@ -4,6 +4,7 @@
 #include "tq_device.cuh"
 
 constexpr int kB8Block = 32;
+constexpr float kB8Inv127 = 1.f / 127.f;               // rounded to fp32; 127 times it rounds to 1
 constexpr float kB8MinMax = 7.8886090522101181e-31f;   // 2^-100: a block whose largest |x| is below it is stored as zeros
 
 static inline int b8_padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
         }
         const float a = __uint_as_float(m << 16);
         const bool live = a >= kB8MinMax;
-        const float inv = live ? 127.f / a : 0.f, scale = live ? a / 127.f : 0.f;
+        const float inv = live ? (1.f / a) * 127.f : 0.f, scale = live ? a * kB8Inv127 : 0.f;
         if (page) {
             uint8_t* rows = b8_codes(c, page, h, side);
 #pragma unroll

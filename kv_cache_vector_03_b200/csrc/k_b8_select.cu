@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
             }
             am = tq_warp_max(am);
             const bool live = __all_sync(0xffffffffu, fin) && am >= kB8MinMax;
-            const float inv = live ? 127.f / am : 0.f;
+            const float inv = live ? (1.f / am) * 127.f : 0.f;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 const int e = lane * (D / 32) + k;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
                 reinterpret_cast<int8_t*>(s_q[w])[e] = (int8_t)min(qi, 0);
                 reinterpret_cast<int8_t*>(s_q[w])[D + e] = (int8_t)max(qi, 0);
             }
-            if (lane == 0) s_step[w] = live ? am / 127.f : 0.f;
+            if (lane == 0) s_step[w] = live ? am * kB8Inv127 : 0.f;
         }
         __syncthreads();
         int acc[4] = {0, 0, 0, 0};
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
             m = fmaxf(m, fabsf(__uint_as_float(__byte_perm(u[k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f));
 #pragma unroll
         for (int o = 1; o < CH; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        top = fmaxf(top, __fmul_rn(m / 127.f, __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
+        top = fmaxf(top, __fmul_rn(__fmul_rn(m, kB8Inv127), __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
     }
     top = tq_warp_max(top);
     if (!dst) return;

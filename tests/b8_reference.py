@@ -6,6 +6,7 @@ from __future__ import annotations
 import numpy as np
 
 BLOCK = 32
+INV127 = np.float32(1) / np.float32(127)
 
 
 def padded(d):
@@ -43,8 +44,8 @@ def quantize(x):
     a = np.float32(np.max(np.abs(x)))
     if a < np.float32(2.0 ** -100):
         return np.zeros(x.shape, int), np.float32(0), bool(fin.all())
-    inv = np.float32(127) / a
-    return np.rint(x * np.float64(inv)).astype(int), a / np.float32(127), bool(fin.all())
+    inv = np.float32(1) / a * np.float32(127)
+    return np.rint(x * np.float64(inv)).astype(int), a * INV127, bool(fin.all())
 
 
 def page_of(kc, ks, vc, vs):
@@ -178,8 +179,8 @@ def select(seq, q, n_sel, nf, nl):
                 x = q[i, h, j]
                 a = np.float32(np.max(np.abs(x))) if np.isfinite(x).all() else np.float32(0)
                 live = a >= np.float32(2.0 ** -100)
-                qi = np.rint(x * np.float64(np.float32(127) / a)) if live else np.zeros(d)
-                step = a / np.float32(127) if live else np.float32(0)
+                qi = np.rint(x * np.float64(np.float32(1) / a * np.float32(127))) if live else np.zeros(d)
+                step = a * INV127 if live else np.float32(0)
                 for b in range(nb):
                     kc = seq.blocks[b][0][h, 0]
                     whole = np.maximum(qi * kc.min(axis=0), qi * kc.max(axis=0)).sum()
@@ -206,7 +207,7 @@ def evict(seq, acc, keep, nf, nl):
             for side in range(2):
                 code = np.stack([seq.blocks[t // BLOCK][0][h, side, t % BLOCK] for t in src])
                 sc = np.array([seq.blocks[t // BLOCK][1][h, side] for t in src], np.float32)
-                top = np.abs(code).max(axis=1).astype(np.float32) / np.float32(127) * sc
+                top = np.abs(code).max(axis=1).astype(np.float32) * INV127 * sc
                 s = top.max()
                 ratio = sc / s if s > 0 else np.zeros(BLOCK, np.float32)
                 new.blocks[j][0][h, side] = np.rint(code * ratio.astype(np.float64)[:, None]).astype(int)
