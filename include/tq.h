@@ -368,7 +368,8 @@ int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dty
  * p = len - n_q + i, already appended) and each query head j, with kv head j / g,
  *   out = sum_t w_t v_t,  w = softmax over t <= p of scale <q, k_t>.
  * A query whose position is negative, or that sees no token, gives zeros.
- *   q         device [n_seq, n_q, n_kv * g, d], fp32 or bf16; n_q, g >= 1, n_q * g <= 16384.
+ *   q         device [n_seq, n_q, n_kv * g, d], fp32 or bf16, 16-byte aligned; n_q, g >= 1,
+ *             n_q * g <= 16384.
  *   sel       device int32 [n_seq, n_q, n_kv, n_sel] block numbers from tq_b8_select: the query
  *             sees only tokens of these blocks and of the open block; entries outside the
  *             full blocks are passed over; an entry that is named twice counts twice. NULL with

@@ -69,7 +69,7 @@ struct B8AttnParams {
     B8Cache c;
     const void* q;
     int q_dtype, n_q, g;
-    float scale;
+    float scale_hi, scale_lo;   // scale * log2(e) as two floats
     const int32_t* sel;
     int n_sel;
     const float* acc_in;
@@ -79,6 +79,9 @@ struct B8AttnParams {
     float* logits;           // [n_seq * n_kv][n_q * g][logit_row] log2-domain logits, when acc_out is asked for
     float* lse;              // [n_seq * n_kv][n_q * g]
     int64_t logit_row;
+    float* part;             // [2 grid][row_tile][D] partial value sums, [2 grid][row_tile][2] their maximum and sum
+    float* part_ml;
+    int grid, row_tile, row_tiles;
 };
 struct B8SelectParams {
     B8Cache c;
@@ -97,6 +100,8 @@ struct B8EvictParams {
     float* acc_out;
 };
 
+int b8_attn_row_tile(int D, int rows);   // query rows a unit is computed for at once
+int b8_attn_grid();                      // CTAs of one wave
 cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st);
 cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st);
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st);

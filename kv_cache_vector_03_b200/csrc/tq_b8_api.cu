@@ -59,7 +59,7 @@ B8Cache view(const tq_b8_cache* c, void* ws) {
 }
 
 // regions after the status word; a call uses those of its own kind, so they share the space
-struct B8Ws { size_t key, lse, logits, total; int64_t logit_row; };
+struct B8Ws { size_t key, part, ml, lse, logits, total; int64_t logit_row; };
 B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     B8Ws w = {};
     const size_t rows = (size_t)c->n_seq * c->n_kv * (size_t)n_q;
@@ -67,6 +67,10 @@ B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     w.key = off;
     const size_t select_end = align_up(off + (n_sel ? rows * (size_t)c->max_blocks * 4 : 0));
     w.logit_row = n_sel ? (int64_t)(n_sel + 1) * kB8Block : c->max_blocks * kB8Block;
+    const int tile = b8_attn_row_tile(b8_padded(c->d), n_sel ? g : n_q * g);
+    const size_t slots = rows && g ? 2 * (size_t)b8_attn_grid() * tile : 0;
+    w.part = off; off = align_up(off + slots * b8_padded(c->d) * 4);
+    w.ml = off; off = align_up(off + slots * 8);
     w.lse = off; off = align_up(off + (weights ? rows * g * 4 : 0));
     w.logits = off; off = align_up(off + (weights ? rows * g * (size_t)w.logit_row * 4 : 0));
     w.total = std::max(select_end, off);
@@ -137,7 +141,7 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     if (acc_in && !acc_out) return TQ_ERR_ARG;
     if (sel && acc_out && n_q != 1) return TQ_ERR_UNSUPPORTED;
     if (c->n_seq == 0) return TQ_OK;
-    if (!q || !out || !aligned(q, q_dtype == TQ_F32 ? 4 : 2) || !aligned(out, 16) || !aligned(sel, 4) ||
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) ||
         !aligned(acc_in, 4) || !aligned(acc_out, 4))
         return TQ_ERR_ARG;
     const B8Ws W = b8_ws(c, n_q, g, n_sel, acc_out != nullptr);
@@ -146,13 +150,21 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     B8AttnParams p;
     std::memset(&p, 0, sizeof(p));
     p.c = view(c, ws);
-    p.q = q; p.q_dtype = q_dtype; p.n_q = n_q; p.g = g; p.scale = scale;
+    p.q = q; p.q_dtype = q_dtype; p.n_q = n_q; p.g = g;
+    const double scale2 = (double)scale * 1.4426950408889634074;   // log2(e)
+    p.scale_hi = (float)scale2;
+    p.scale_lo = std::isfinite(p.scale_hi) ? (float)(scale2 - (double)p.scale_hi) : 0.f;
     p.sel = sel; p.n_sel = n_sel;
     p.acc_in = acc_in; p.acc_out = acc_out; p.decay = decay;
     p.out = out;
     p.lse = reinterpret_cast<float*>(wsb + W.lse);
     p.logits = reinterpret_cast<float*>(wsb + W.logits);
     p.logit_row = W.logit_row;
+    p.part = reinterpret_cast<float*>(wsb + W.part);
+    p.part_ml = reinterpret_cast<float*>(wsb + W.ml);
+    p.grid = b8_attn_grid();
+    p.row_tile = b8_attn_row_tile(p.c.D, sel ? g : n_q * g);
+    p.row_tiles = ((sel ? g : n_q * g) + p.row_tile - 1) / p.row_tile;
     return cuda_status(b8_launch_attention(p, static_cast<cudaStream_t>(stream)));
 }
 
