@@ -26,19 +26,20 @@ namespace {
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kBias = 7.f;         // weights are kept as 2^(7 + logit - m): their small pieces stay normal in fp16
 constexpr float kSlack = 8.f;        // m follows the maximum once it is passed by 2^8: 2^(7 + 8) < 65504
-constexpr int kMinUnits = 8;         // units a CTA takes at least
+constexpr int kMinUnits = 16;        // units a CTA takes at least, where segments are shared
+constexpr int kStraddle = 24;
+constexpr int kWholeUnits = 32;      // segments up to here are not shared
 constexpr int kAccTok = 256;
 
-template <int D>
-struct Ring {
-    static constexpr int warps = D == 256 ? 4 : 8;
-    static constexpr int stages = D == 64 ? 4 : 2;
-    static constexpr int stage_bytes = 64 * D + 128;   // keys, values, scales
-};
+// Warps, the CTA's ring of pages, and in how many rounds the warps' sums meet in shared memory
 template <int D, int NT>
-constexpr size_t smem_bytes() {
-    return (size_t)Ring<D>::warps * (Ring<D>::stages * Ring<D>::stage_bytes + 8 * NT * D * 4);
-}
+struct Shape {
+    static constexpr int warps = D == 256 ? 8 : NT == 2 && D == 128 ? 12 : 16;
+    static constexpr int stages = D == 64 ? 40 : D == 128 ? 20 : 10;
+    static constexpr int stage_bytes = 64 * D + 128;   // keys, values, scales
+    static constexpr int rounds = NT * D == 64 ? 1 : NT * D == 128 ? 2 : D == 256 ? 2 : 4;
+    static constexpr size_t smem = (size_t)stages * stage_bytes + (size_t)warps * 8 * NT * (D / rounds + 4) * 4;
+};
 
 TQ_DEVICE uint32_t h2sub(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -65,264 +66,379 @@ TQ_DEVICE uint32_t transpose8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-TQ_DEVICE void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// The accumulator comes in and goes out separately, so that a chain starts from any register (or zero); not
+// volatile, so that chains interleave.
+#define B8_MMA(NAME, KIND, T, R)                                                                                        \
+    TQ_DEVICE void NAME(T (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, T c0,  \
+                        T c1, T c2, T c3) {                                                                             \
+        asm("mma.sync.aligned." KIND " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"                        \
+            : "=" R(d[0]), "=" R(d[1]), "=" R(d[2]), "=" R(d[3])                                                        \
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), R(c0), R(c1), R(c2), R(c3));                        \
+    }                                                                                                                   \
+    TQ_DEVICE void NAME(T (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {      \
+        NAME(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);                                                        \
+    }
+B8_MMA(mma_f16, "m16n8k16.row.col.f32.f16.f16.f32", float, "f")
+B8_MMA(mma_bf16, "m16n8k16.row.col.f32.bf16.bf16.f32", float, "f")
+B8_MMA(mma_u8s8, "m16n8k32.row.col.s32.u8.s8.s32", int, "r")
+#undef B8_MMA
+TQ_DEVICE uint32_t atomic_add_acq_rel(uint32_t* at, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(v) : "memory");
+    return old;
 }
 
 // ------------------------------------------------------------------------ the list of units
-// "virtual sequences": a sequence, or with a selection one query token of it
+// "virtual sequences": a sequence, or with a selection one query token of it. The host has checked that
+// all units together, and the units of one virtual sequence over all heads and tiles, count below 2^30.
+TQ_DEVICE int virt_units(const B8AttnParams& p, int v, int& n) {
+    const int s = p.sel && p.n_q > 1 ? v / p.n_q : v;
+    n = b8_len(p.c, s);
+    const int open = ((n & 31) + 15) / 16;
+    if (!p.sel) return (n >> 5) + open;
+    return n - p.n_q + (v - s * p.n_q) < 0 ? 0 : p.n_sel + open;
+}
 struct Plan {
-    int64_t total, u0, u1, n_virt;
-    int ctas;
+    int u0, mine;                // this CTA's units begin at u0 (counted over the whole list), mine of them
+    int virt, x;                 // u0 is unit x of virtual sequence virt
+    int c0, c1;                  // the CTAs that share this CTA's only segment, or c0 = -1: ask owner()
+    int base, extra;             // equal shares: base units, one more for the first `extra` CTAs
+    TQ_DEVICE int share(int c) const { return c * base + min(c, extra); }
+    TQ_DEVICE int owner(int u) const {
+        const int wide = extra * (base + 1);
+        return u < wide ? u / (base + 1) : extra + (u - wide) / base;
+    }
 };
-TQ_DEVICE int virt_units(const B8AttnParams& p, int64_t v, int& n) {
-    if (!p.sel) {
-        n = b8_len(p.c, v);
-        return (n >> 5) + ((n & 31) ? 1 : 0);
-    }
-    n = b8_len(p.c, v / p.n_q);
-    return n - p.n_q + (int)(v % p.n_q) < 0 ? 0 : p.n_sel + ((n & 31) ? 1 : 0);
-}
+// Sums the units of all virtual sequences and finds this CTA's share of them, one of three ways:
+//   segments of up to kWholeUnits units: shares begin and end between segments, nothing is joined;
+//   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length. A CTA
+//     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
+//     everyone would wait for it;
+//   else equal shares, cut where they fall.
 template <int THREADS>
-TQ_DEVICE int64_t block_scan(int64_t x, int64_t* s, int64_t& total) {   // inclusive; s: THREADS / 32 words
+TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) {
+    constexpr int NW = THREADS / 32;
+    __shared__ int s_sum[NW], s_max[NW], s_at[2][3];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int all;                                         // the sum over the block
+    auto scan = [&](int x) {                         // inclusive sum up to this thread
+        int incl = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s[w] = x;
-    __syncthreads();
-    total = 0;
-    int64_t before = 0;
-#pragma unroll
-    for (int k = 0; k < THREADS / 32; ++k) {
-        if (k < w) before += s[k];
-        total += s[k];
-    }
-    return x + before;
-}
-TQ_DEVICE int64_t share(const Plan& pl, int c) { return pl.total * c / pl.ctas; }
-TQ_DEVICE int owner(const Plan& pl, int64_t u) { return (int)(((u + 1) * pl.ctas - 1) / pl.total); }
-
-template <int THREADS>
-TQ_DEVICE void plan_total(const B8AttnParams& p, Plan& pl, int64_t* s) {
-    pl.n_virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
-    pl.total = 0;
-    for (int64_t v0 = 0; v0 < pl.n_virt; v0 += THREADS) {
-        const int64_t v = v0 + threadIdx.x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[w] = incl;
+        __syncthreads();
+        const int sw = lane < NW ? s_sum[lane] : 0;
+        all = (int)__reduce_add_sync(0xffffffffu, sw);
+        return incl + (int)__reduce_add_sync(0xffffffffu, lane < w ? sw : 0);
+    };
+    auto units_of = [&](int v) {
         int n;
-        int64_t sum;
-        block_scan<THREADS>(v < pl.n_virt ? (int64_t)virt_units(p, v, n) * p.c.n_kv * p.row_tiles : 0, s, sum);
-        pl.total += sum;
+        return v < n_virt ? virt_units(p, v, n) : 0;
+    };
+    int total = 0, longest = 0, units = 0, incl = 0;
+#pragma unroll 1
+    for (int v0 = 0; v0 < n_virt; v0 += THREADS) {
+        units = units_of(v0 + threadIdx.x);
+        longest = max(longest, units);
+        incl = scan(units * segs);
+        total += all;
     }
-    const int64_t most = (pl.total + kMinUnits - 1) / kMinUnits;
-    pl.ctas = (int)(most < p.grid ? (most > 1 ? most : 1) : p.grid);
+    longest = (int)__reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) s_max[w] = longest;
+    pl.u0 = pl.mine = 0;
+    pl.c0 = -1;
+    if (total == 0) return;
+    __syncthreads();
+    longest = (int)__reduce_max_sync(0xffffffffu, lane < NW ? s_max[lane] : 0);
+    const bool one = n_virt <= THREADS;              // units and incl are this thread's virtual sequence's
+    const bool whole = longest <= kWholeUnits;
+    const int n_segs = n_virt * segs;
+    if (!whole && n_segs <= p.grid) {                // (then n_virt <= THREADS)
+        // 1 + floor(units (grid - segments) / total) parts each are never more than the grid together
+        const int spare = min(p.grid, total / kMinUnits) - n_segs;
+        const int parts = units ? 1 + (spare > 0 ? (int)((uint32_t)units * (uint32_t)spare / (uint32_t)total) : 0) : 0;
+        const int upto = scan(parts * segs), b = blockIdx.x;
+        const int most = __syncthreads_or(units > parts * (total / p.grid + kStraddle));
+        if (!most) {
+            if (b >= all) return;
+            if (upto - parts * segs <= b && b < upto) {
+                const int j = b - (upto - parts * segs), seg = j / parts, part = j - seg * parts;
+                const int wide = units / parts, extra = units - wide * parts;
+                s_at[0][0] = threadIdx.x;
+                s_at[0][1] = seg * units + part * wide + min(part, extra);
+                s_at[0][2] = wide + (part < extra ? 1 : 0);
+                s_at[1][0] = b - part;
+                s_at[1][1] = b - part + parts - 1;
+            }
+            __syncthreads();
+            pl.virt = s_at[0][0];
+            pl.x = s_at[0][1];
+            pl.mine = s_at[0][2];
+            pl.c0 = s_at[1][0];
+            pl.c1 = s_at[1][1];
+            return;
+        }
+    }
+    const int ctas = min(p.grid, whole ? min(total, n_virt * segs) : max(1, total / kMinUnits));
+    pl.base = total / ctas;
+    pl.extra = total - pl.base * ctas;
+    if ((int)blockIdx.x >= ctas) return;
+    const int lo = pl.share(blockIdx.x), hi = pl.share(blockIdx.x + 1);
+    if (one) incl = scan(units * segs);
+#pragma unroll 1
+    for (int v0 = 0, base = 0;; v0 += THREADS) {
+        if (!one) {
+            units = units_of(v0 + threadIdx.x);
+            incl = scan(units * segs);
+        }
+        const int before = base + incl - units * segs;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int u = k ? hi : lo;
+            if (before <= u && u < base + incl) {
+                int off = u - before;
+                if (whole) off -= off % units;
+                s_at[k][0] = v0 + threadIdx.x;
+                s_at[k][1] = off;
+                s_at[k][2] = before + off;
+            }
+        }
+        base += all;
+        if (base > hi || base >= total) break;
+    }
+    __syncthreads();
+    pl.virt = s_at[0][0];
+    pl.x = s_at[0][1];
+    pl.u0 = s_at[0][2];
+    pl.mine = (hi < total ? s_at[1][2] : total) - pl.u0;
 }
 
-template <int D, int NT, int QP>
-__global__ void __launch_bounds__(Ring<D>::warps * 32, 1) k_b8_attn(const __grid_constant__ B8AttnParams p) {
-    constexpr int NW = Ring<D>::warps, ST = Ring<D>::stages, SB = Ring<D>::stage_bytes;
-    constexpr int KC = D / 64;           // 16-byte key chunks of a lane per token
+template <int D>
+TQ_DEVICE int channel(int gq, int mt, int y) {   // the channel of row gq + 8 y of O^T's m-tile mt
+    return D == 256 ? 16 * (gq + 8 * (mt >> 3)) + 2 * (mt & 7) + y : gq * (D / 8) + 2 * mt + y;
+}
+
+// a unit's page: where its codes and its scales are; or half of an open block: where its keys and values are
+struct __align__(8) Record {
+    const uint8_t* a;
+    const uint8_t* b;
+    int what;                                        // 0 a page, -1 nothing, -2, -3 a half of the open block
+    int block;
+};
+
+template <int D, int NT, bool WT>
+__global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const __grid_constant__ B8AttnParams p) {
+    using Sh = Shape<D, NT>;
+    constexpr int NW = Sh::warps, ST = Sh::stages, SB = Sh::stage_bytes, RD = Sh::rounds;
     constexpr int MT = D / 16;           // m-tiles of O^T
     constexpr int VW = D / 32;           // value words (4 channels) of a lane per token
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_full[NW * ST];
-    __shared__ int64_t s_scan[NW], s_start[2];
-    __shared__ float s_m[NW][8 * NT], s_l[NW][8 * NT];
+    __shared__ __align__(8) uint64_t s_full[ST];
+    __shared__ int2 s_meta[ST];                      // what a stage holds, and its block
+    __shared__ int s_unit[ST];                       // and of which unit
+    __shared__ Record s_rec[NW][32];
+    __shared__ float2 s_ml[8 * NT][NW];              // the warps' maxima and sums
+    __shared__ float s_fac[8 * NT][NW], s_top[8 * NT], s_sum[8 * NT], s_f[8 * NT];
+    __shared__ int s_last;
+    __shared__ uint2 s_q[NT * 3 * (D / 32) * 32];     // q as B fragments, three int8 pieces
+    __shared__ int s_qsum[3][8 * NT];                // -128 times the sum of a row's piece, + the bits of 1.5 * 2^23
+    float* s_o = reinterpret_cast<float*>(smem + (size_t)ST * SB);
     const B8Cache& c = p.c;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    uint8_t* ring = smem + (size_t)w * ST * SB;
-    float* s_o = reinterpret_cast<float*>(smem + (size_t)NW * ST * SB);
-    if (lane < ST) tq_mbar_init(&s_full[w * ST + lane], 2);
+    if (threadIdx.x < ST) {
+        tq_mbar_init(&s_full[threadIdx.x], 1);
+        s_unit[threadIdx.x] = -1;
+    }
     tq_fence_mbar_init();
     tq_pdl_launch_dependents();
 
-    Plan pl;
-    plan_total<NW * 32>(p, pl, s_scan);
-    if ((int)blockIdx.x >= pl.ctas || pl.total == 0) return;
-    pl.u0 = share(pl, blockIdx.x);
-    pl.u1 = share(pl, blockIdx.x + 1);
     const int segs = c.n_kv * p.row_tiles;
-    {
-        int64_t base = 0;
-        for (int64_t v0 = 0; v0 < pl.n_virt; v0 += NW * 32) {
-            const int64_t v = v0 + threadIdx.x;
-            int n;
-            int64_t sum;
-            const int64_t x = v < pl.n_virt ? (int64_t)virt_units(p, v, n) * segs : 0;
-            const int64_t before = base + block_scan<NW * 32>(x, s_scan, sum) - x;
-            if (before <= pl.u0 && pl.u0 < before + x) {
-                s_start[0] = v;
-                s_start[1] = pl.u0 - before;
+    const int n_virt = (int)(p.sel ? c.n_seq * p.n_q : c.n_seq);
+    const int rows = p.sel ? p.g : p.n_q * p.g;      // query rows of a virtual sequence and kv head
+    auto q_row = [&](int v, int h, int r) {
+        const int t = p.sel ? 0 : r / p.g;           // query token within the virtual sequence
+        return ((int64_t)v * (p.sel ? 1 : p.n_q) + t) * c.n_kv * p.g + h * p.g + r - t * p.g;
+    };
+    Plan pl;
+    make_plan<NW * 32>(p, n_virt, segs, pl);
+    // rows of sequences without a token are zeros
+#pragma unroll 1
+    for (int v = blockIdx.x; v < n_virt; v += gridDim.x) {
+        int n;
+        if (virt_units(p, v, n) == 0) {
+#pragma unroll 1
+            for (int hr = w; hr < c.n_kv * rows; hr += NW) {
+                float* out = p.out + q_row(v, hr / rows, hr % rows) * c.d;
+                for (int e = lane; e < c.d; e += 32) out[e] = 0.f;
+                if (WT && lane == 0) p.lse[(int64_t)v * c.n_kv * rows + hr] = INFINITY;
             }
-            base += sum;
-            if (base > pl.u0) break;
+        }
+    }
+    const int mine = pl.mine;
+    if (mine <= 0) return;
+
+    // Unit i of the share goes to warp i mod NW and stage i mod ST; who has consumed a stage refills it with
+    // unit i + ST. The k-th unit that this warp issues is a(k) = w + NW k for the first `early` ones, which it
+    // issues before it has consumed any, then w + ST + NW (k - early). Lane l looks up a(l), a(l + 32), ..., whose
+    // records stand in rec[k mod 32]; 16 at a time are looked up when the 16 before them have been used.
+    const int early = (ST - w + NW - 1) / NW;
+    int fi = lane < early ? w + NW * lane : w + ST + NW * (lane - early), fv = pl.virt, fx = pl.x + fi;
+    Record* rec = s_rec[w];
+    auto fetch = [&](int to) {
+        Record r = {nullptr, nullptr, -1, 0};
+        if (fi < mine) {
+            int n, units;
+#pragma unroll 1
+            while (fx >= (units = virt_units(p, fv, n)) * segs) {
+                fx -= units * segs;
+                ++fv;
+            }
+            const int seg = fx / units, off = fx - seg * units, pages = p.sel ? p.n_sel : n >> 5;
+            const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, s = p.sel && p.n_q > 1 ? fv / p.n_q : fv;
+            if (off >= pages) {
+                const uint16_t* k = b8_open(c, s, h, 0) + 16 * (off - pages) * c.d;
+                r = {reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(k + 32 * c.d), -2 - (off - pages), n >> 5};
+            } else {
+                r.block = p.sel ? p.sel[((int64_t)fv * c.n_kv + h) * p.n_sel + off] : off;
+                if (r.block >= 0 && r.block < (n >> 5)) {
+                    const uint8_t* page = b8_page(c, c.table[(int64_t)s * c.max_blocks + r.block]);
+                    if (page) r = {page + c.header_bytes + (size_t)h * (64 * D), page + (size_t)h * (32 + 2 * D), 0, r.block};
+                }
+            }
+        }
+        rec[lane] = r;
+        fx += to - fi;
+        fi = to;
+    };
+    bool ok = true;                                  // no wait of this warp has run out
+    int issued = 0;
+    auto issue = [&](int i, int st) {                // i = a(issued), st = i mod ST
+        if (!ok || i >= mine) return;
+        if ((issued & 15) == 0) {
+            const bool all = issued == 0;
+            __syncwarp();
+            if (all || (lane >> 4) == ((issued >> 4) - 1 & 1)) fetch(all ? w + ST + NW * (32 + lane - early) : fi + 32 * NW);
+            __syncwarp();
+        }
+        if (lane == 0) {
+            const Record r = rec[issued & 31];
+            s_meta[st] = make_int2(r.what, r.block);
+            *const_cast<volatile int*>(&s_unit[st]) = i;
+            uint8_t* dst = smem + (size_t)st * SB;
+            if (r.what == -1)
+                tq_mbar_arrive(&s_full[st]);
+            else if (r.what == 0)
+                tq_bulk_load2(dst, r.a, 64 * D, dst + 64 * D, r.b, 16, &s_full[st]);
+            else
+                tq_bulk_load2(dst, r.a, 32 * c.d, dst + 32 * D, r.b, 32 * c.d, &s_full[st]);
+        }
+        ++issued;
+    };
+
+    int i = w, v = pl.virt, x0 = pl.x;               // i: this warp's next unit, in stage st
+    int st = w % ST;
+    uint32_t phase = 0;
+    // where a lane's values (tokens 2 tq, 2 tq + 1) lie in a page; 8 tokens on is 8 D on
+    const uint32_t sv0 = b8_swz(2 * tq, D / 16), sv1 = b8_swz(2 * tq + 1, D / 16);
+    const uint32_t vch = D == 64 ? gq >> 1 : gq, vhalf = D == 64 ? (gq & 1) * 8 : 0;
+    // ldmatrix: lane l gives the row address of token l mod 16, chunk l / 16 (of a pair; pair x is 32 x bytes on, an
+    // exclusive or since the swizzle is one)
+    const uint32_t at_k = (lane & 15) * D + (((lane >> 4) ^ b8_swz(lane & 15, D / 16)) << 4);
+    const uint32_t at_v0 = 32 * D + 2 * tq * D + ((vch ^ sv0) << 4) + vhalf, at_v1 = 32 * D + (2 * tq + 1) * D + ((vch ^ sv1) << 4) + vhalf;
+    for (int u = 0; u < mine;) {
+        int n, units;
+#pragma unroll 1
+        while (x0 >= (units = virt_units(p, v, n)) * segs) {
+            x0 -= units * segs;
+            ++v;
+        }
+        const int seg = x0 / units, off = x0 - seg * units;
+        const int part = min(units - off, mine - u);
+        const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * 8 * NT;
+        const int s = p.sel && p.n_q > 1 ? v / p.n_q : v;
+        const int all_see = n - p.n_q + (p.sel ? v - s * p.n_q : 0);          // every row sees the positions up to here
+
+        if (u == 0) {
+#pragma unroll 1
+            for (int k = 0; k < early; ++k) issue(w + NW * k, w + NW * k);
+        }
+        // q, while the first pages are on their way: a warp per row, a lane per 4 channels. A row is scaled by a
+        // power of two to below 2^22 and rounded to a whole number, which three int8 pieces hold.
+#pragma unroll 1
+        for (int r = w; r < 8 * NT; r += NW) {
+            constexpr int Q4 = D == 256 ? 2 : 1;
+            float4 q[Q4];
+            uint32_t top = 0;
+            const int64_t at = row0 + r < rows ? q_row(v, h, row0 + r) * c.d : 0;
+#pragma unroll
+            for (int k = 0; k < Q4; ++k) {
+                const int e = 4 * (lane + 32 * k);
+                q[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row0 + r < rows && e < c.d) {
+                    if (p.q_dtype) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at + e);
+                        q[k] = make_float4(bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y));
+                    } else {
+                        q[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e);
+                    }
+                }
+                top = max(max(top, max(__float_as_uint(q[k].x) & 0x7fffffffu, __float_as_uint(q[k].y) & 0x7fffffffu)),
+                          max(__float_as_uint(q[k].z) & 0x7fffffffu, __float_as_uint(q[k].w) & 0x7fffffffu));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int eb = min(max((int)(top >> 23), 27), 254);
+            // 2^(148 - eb), or 0 for a row that is not finite, which answers NaN
+            const float up = top >= 0x7f800000u ? 0.f : __uint_as_float((uint32_t)(275 - eb) << 23);
+            int sum[3] = {0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < Q4; ++k) {
+                const float f[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+                uint32_t word[3] = {0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int x = __float2int_rn(f[j] * up), hi = (x + 32896) >> 16, y = x - (hi << 16);
+                    const int piece[3] = {hi, (y + 128) >> 8, y - (((y + 128) >> 8) << 8)};
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) {
+                        word[z] |= (uint32_t)(piece[z] & 0xff) << (8 * j);
+                        sum[z] += piece[z];
+                    }
+                }
+                const int id = lane + 32 * k;             // channels 4 id .. + 3: k-step id / 8, register id / 4 mod 2, lane id mod 4
+                if (id < D / 4)
+#pragma unroll
+                    for (int z = 0; z < 3; ++z)
+                        reinterpret_cast<uint32_t*>(s_q)[((((r >> 3) * 3 + z) * (D / 32) + (id >> 3)) * 32 + (r & 7) * 4 + (id & 3)) * 2 +
+                                                         (id >> 2 & 1)] = word[z];
+            }
+#pragma unroll
+            for (int z = 0; z < 3; ++z) sum[z] = (int)__reduce_add_sync(0xffffffffu, sum[z]);
+            if (lane < 3) s_qsum[lane][r] = 0x4b400000 - 128 * (lane == 0 ? sum[0] : lane == 1 ? sum[1] : sum[2]);
+            if (lane == 0) s_f[r] = up == 0.f ? NAN : __uint_as_float((uint32_t)(eb - 21) << 23);
         }
         __syncthreads();
-    }
-
-    // this warp's units, NW apart: lane l of a batch holds where unit 32 batch + l lies
-    int64_t fv = s_start[0], fx = s_start[1] + w + NW * lane, fu = pl.u0 + w + NW * lane;
-    int name = -1, blk = -1, head = 0, next_name = -1, next_blk = -1, next_head = 0;
-    auto fetch = [&](int& rname, int& rblk, int& rhead) {
-        rname = rblk = -1;
-        rhead = 0;
-        if (fu < pl.u1) {
-            int n, units = virt_units(p, fv, n);
-            while (fx >= (int64_t)units * segs) {
-                fx -= (int64_t)units * segs;
-                units = virt_units(p, ++fv, n);
-            }
-            const int seg = (int)(fx / units), off = (int)(fx - (int64_t)seg * units);
-            const int64_t s = p.sel ? fv / p.n_q : fv;
-            rhead = seg / p.row_tiles;
-            if ((n & 31) && off == units - 1) {
-                rname = -2;
-                rblk = n >> 5;
-            } else {
-                rblk = p.sel ? p.sel[(fv * c.n_kv + rhead) * p.n_sel + off] : off;
-                if (rblk >= 0 && rblk < (n >> 5)) {
-                    rname = c.table[s * c.max_blocks + rblk];
-                    if (rname < 0 || rname >= c.n_pages) {
-                        tq_raise(c.status, TQ_FLAG_RANGE);
-                        rname = -1;
-                    }
-                }
-            }
-        }
-        fu += 32 * NW;
-        fx += 32 * NW;
-    };
-    const int mine = (int)((pl.u1 - pl.u0 - w + NW - 1) / NW);   // this warp's units (none: <= 0)
-    uint32_t in_flight = 0, phase = 0;                           // a bit per stage
-    auto issue = [&](int i) {                                    // i counts up from 0, once each
-        if ((i & 31) == 0) {
-            if (i == 0) fetch(name, blk, head);
-            else { name = next_name; blk = next_blk; head = next_head; }
-            fetch(next_name, next_blk, next_head);
-        }
-        const int nm = __shfl_sync(0xffffffffu, name, i & 31), h = __shfl_sync(0xffffffffu, head, i & 31);
-        if (nm < 0) return;
-        const int st = i % ST;
-        in_flight |= 1u << st;
-        if (lane == 0) {
-            const uint8_t* page = c.pages + (size_t)nm * c.page_bytes;
-            uint8_t* dst = ring + st * SB;
-            tq_bulk_load(dst, page + c.header_bytes + (size_t)h * (64 * D), 64 * D, &s_full[w * ST + st]);
-            tq_bulk_load(dst + 64 * D, page + (size_t)h * (32 + 2 * D), 16, &s_full[w * ST + st]);
-        }
-    };
-    __syncwarp();
-    bool ok = true;                                              // no wait of this warp has run out
-    // a batch changes while units of the last one are in flight, so what a unit is stays with its stage
-    int kind[ST], where[ST];
-    auto stage_in = [&](int i) {
-        const int st = i % ST;
-        if (ok && i < mine) issue(i);
-        const int k = __shfl_sync(0xffffffffu, name, i & 31), b = __shfl_sync(0xffffffffu, blk, i & 31);
-#pragma unroll
-        for (int x = 0; x < ST; ++x)
-            if (x == st) {
-                kind[x] = k;
-                where[x] = b;
-            }
-    };
-#pragma unroll
-    for (int i = 0; i < ST; ++i) stage_in(i);
-
-    int i = 0;
-    int64_t v = s_start[0], x0 = s_start[1];
-    for (int64_t u = pl.u0; u < pl.u1;) {
-        int n, units = virt_units(p, v, n);
-        while (x0 >= (int64_t)units * segs) {
-            x0 -= (int64_t)units * segs;
-            units = virt_units(p, ++v, n);
-        }
-        const int seg = (int)(x0 / units), off = (int)(x0 - (int64_t)seg * units);
-        const int part = (int)min((int64_t)(units - off), pl.u1 - u);
-        const int h = seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * 8 * NT;
-        const int64_t s = p.sel ? v / p.n_q : v;
-        const int first_q = p.sel ? (int)(v - s * p.n_q) : 0;
-        const int rows = p.sel ? p.g : p.n_q * p.g;
-        const int64_t qbase = (s * p.n_q + first_q) * c.n_kv * p.g + (int64_t)h * p.g;   // row of query row 0
-        auto q_row = [&](int r) { return qbase + (int64_t)(r / p.g) * c.n_kv * p.g + r % p.g; };
-
-        // q as B fragments: row gq of each n-tile, channels 16 (tq + 4 c) + 4 k .. + 3
-        uint32_t qf[NT][QP][KC * 4][2];
         float fh[NT][2], fl[NT][2];      // logits factor (key scale aside) of rows 2 tq, 2 tq + 1
-        int last[NT][2];                 // the last position that these rows see
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + 8 * nt + gq;
-            float q[KC * 16];
-            uint32_t top = 0;
-            const int64_t at = r < rows ? q_row(r) * c.d : 0;
-#pragma unroll
-            for (int k = 0; k < KC * 2; ++k) {
-                const int e = 16 * (tq + 4 * (k >> 1)) + 8 * (k & 1);
-                if (r < rows && e < c.d) {
-                    if (QP == 1) {
-                        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + e);
-                        const uint32_t u4[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            q[8 * k + 2 * j] = bf_lo(u4[j]);
-                            q[8 * k + 2 * j + 1] = bf_hi(u4[j]);
-                        }
-                    } else {
-                        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e);
-                        const float4 a = f[0], b = f[1];
-                        q[8 * k] = a.x; q[8 * k + 1] = a.y; q[8 * k + 2] = a.z; q[8 * k + 3] = a.w;
-                        q[8 * k + 4] = b.x; q[8 * k + 5] = b.y; q[8 * k + 6] = b.z; q[8 * k + 7] = b.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) q[8 * k + j] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(q[8 * k + j]) & 0x7fffffffu);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int eb = max((int)(top >> 23), 27);
-            const float up = __uint_as_float((uint32_t)(267 - min(eb, 254)) << 23);      // 2^(140 - eb)
-            const float down = __uint_as_float((uint32_t)(min(eb, 254) - 13) << 23);     // 2^(eb - 140)
-#pragma unroll
-            for (int k = 0; k < KC * 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float a = q[4 * k + 2 * e] * up, b = q[4 * k + 2 * e + 1] * up;
-                    qf[nt][0][k][e] = pack_h2(a, b);
-                    if (QP == 2) {
-                        const float2 t = unpack_h2(qf[nt][0][k][e]);
-                        qf[nt][QP - 1][k][e] = pack_h2(a - t.x, b - t.y);
-                    }
-                }
-            const float f0 = eb >= 255 ? NAN : down;     // a row that is not finite answers NaN
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float f = __shfl_sync(0xffffffffu, f0, (2 * tq + e) * 4);
-                fh[nt][e] = f * p.scale_hi;
-                fl[nt][e] = f * p.scale_lo;
-                const int rr = row0 + 8 * nt + 2 * tq + e;
-                last[nt][e] = rr < rows ? n - p.n_q + first_q + rr / p.g : -1;
-            }
-        }
-        const int all_see = n - p.n_q + first_q;         // every row sees the positions up to here
-
         float m[NT][2], l[NT][2], o[MT][NT][4];
+        bool big = false;                // some |m| is beyond 2^16
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const float f = s_f[8 * nt + 2 * tq + e];
+                fh[nt][e] = f * p.scale_hi;
+                fl[nt][e] = f * p.scale_lo;
                 m[nt][e] = -INFINITY;
                 l[nt][e] = 0.f;
             }
+        int sees[NT][2];                   // the last position that these rows see
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sees[nt][e] = p.sel ? all_see : all_see + (row0 + 8 * nt + 2 * tq + e) / p.g;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -330,115 +446,102 @@ __global__ void __launch_bounds__(Ring<D>::warps * 32, 1) k_b8_attn(const __grid
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
 
-        for (int k = (int)((w - (u - pl.u0) % NW + NW) % NW); k < part; k += NW, ++i) {
-            const int st = i % ST;
-            int what = 0, b = 0;
-#pragma unroll
-            for (int x = 0; x < ST; ++x)
-                if (x == st) {
-                    what = kind[x];
-                    b = where[x];
-                }
-            if (what >= 0) {
-                ok = ok && __all_sync(0xffffffffu, tq_mbar_wait(&s_full[w * ST + st], phase >> st & 1u, kWaitLimit));
-                if (ok) {
-                    phase ^= 1u << st;
-                    in_flight &= ~(1u << st);
-                } else {
-                    what = -1;
-                }
-            }
+        for (; i < u + part; i += NW) {
+            // The barrier's parity tells one phase from the next, not from the one after: unit i has to be the
+            // stage's before its phase is waited for, since the warp that refills it may be far behind.
+            for (uint32_t it = 0; ok && *const_cast<volatile int*>(&s_unit[st]) != i; ++it) ok = it < kWaitLimit;
+            ok = __all_sync(0xffffffffu, ok && tq_mbar_wait(&s_full[st], phase, kWaitLimit));
+            const int what = ok ? s_meta[st].x : -1, b = ok ? s_meta[st].y : 0;
             float* lg = nullptr;                          // this unit's logits, [row][logit_row], if they are wanted
-            if (p.acc_out)
-                lg = p.logits + ((s * c.n_kv + h) * (int64_t)(p.n_q * p.g) + row0) * p.logit_row +
-                     (int64_t)(p.sel ? off + k : b) * 32;
+            if (WT) {
+                const int at = off + i - u, pages = p.sel ? p.n_sel : n >> 5;
+                lg = p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0) * p.logit_row +
+                     (at < pages ? 32 * (int64_t)at : 32 * (int64_t)pages + 16 * (at - pages));
+            }
+            if (WT && what == -1)
+                for (int r = 0; r < 8 * NT && row0 + r < rows; ++r) lg[r * p.logit_row + lane] = -INFINITY;
+            if (what != -1) {
             float sc[2][NT][4];                           // S^T: tokens 16 mt + gq (+ 8), rows 2 tq, 2 tq + 1
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-            const uint8_t* kp = ring + st * SB;
+            const uint8_t* kp = smem + (size_t)st * SB;
             const uint8_t* vp = kp + 32 * D;
             float ks = 1.f, vs = 1.f;
-            const int r = n & 31;
+            const int half = -2 - what;                   // of the open block
+            const int left = what >= 0 ? 32 : min(16, (n & 31) - 16 * half), pos0 = what >= 0 ? 32 * b : 32 * b + 16 * half;
             if (what >= 0) {
                 const float2 kv = *reinterpret_cast<const float2*>(kp + 64 * D);
                 ks = kv.x;
                 vs = kv.y;
+                int acc[3][2][NT][4];                     // [piece][token half]: the codes are unsigned, code + 128
 #pragma unroll
-                for (int cc = 0; cc < KC; ++cc) {
-                    uint4 kw[4];
+                for (int x = 0; x < D / 32; ++x) {        // 32 channels: chunks 2 x, 2 x + 1
+                    uint32_t k[2][4];
+                    const uint32_t ka = tq_smem_addr(kp) + (at_k ^ (32 * x));
+                    tq_ldsm_x4(ka, k[0][0], k[0][1], k[0][2], k[0][3]);
+                    tq_ldsm_x4(ka + 16 * D, k[1][0], k[1][1], k[1][2], k[1][3]);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        kw[t] = *reinterpret_cast<const uint4*>(
-                            kp + (gq + 8 * t) * D + (((tq + 4 * cc) ^ b8_swz(gq + 8 * t, D / 16)) << 4));
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t lo[4], hi[4];
+                        for (int z = 0; z < 3; ++z) {
+                            const uint2 q = s_q[((nt * 3 + z) * (D / 32) + x) * 32 + lane];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t word = x == 0 ? kw[t].x : x == 1 ? kw[t].y : x == 2 ? kw[t].z : kw[t].w;
-                            lo[t] = codes_h2<0x4140>(word);
-                            hi[t] = codes_h2<0x4342>(word);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int qp = 0; qp < QP; ++qp) {
-                                const uint32_t* q = qf[nt][qp][cc * 4 + x];
-                                tq_hmma(sc[0][nt], lo[0], lo[1], hi[0], hi[1], q[0], q[1]);
-                                tq_hmma(sc[1][nt], lo[2], lo[3], hi[2], hi[3], q[0], q[1]);
-                            }
-                    }
-                }
-            } else if (what == -2) {
-                // open block: bf16 keys; q again in bf16 pieces (1 holds a bf16 q, 3 hold 22 bits)
-                const uint16_t* kg = b8_open(c, s, h, 0);
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc) {
-                    const int e0 = 16 * (tq + 4 * cc);
-                    uint32_t kw[4][8];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint4 a = make_uint4(0u, 0u, 0u, 0u);
-                            if (gq + 8 * t < r && e0 + 8 * y < c.d)
-                                a = *reinterpret_cast<const uint4*>(kg + (gq + 8 * t) * c.d + e0 + 8 * y);
-                            kw[t][4 * y] = a.x; kw[t][4 * y + 1] = a.y; kw[t][4 * y + 2] = a.z; kw[t][4 * y + 3] = a.w;
-                        }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float a[4];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float2 t = unpack_h2(qf[nt][0][cc * 4 + x][e]);
-                                a[2 * e] = t.x;
-                                a[2 * e + 1] = t.y;
-                                if (QP == 2) {
-                                    const float2 z = unpack_h2(qf[nt][QP - 1][cc * 4 + x][e]);
-                                    a[2 * e] += z.x;
-                                    a[2 * e + 1] += z.y;
+                            for (int mt = 0; mt < 2; ++mt) {
+                                if (x == 0) {
+                                    const int2 y = *reinterpret_cast<const int2*>(&s_qsum[z][8 * nt + 2 * tq]);
+                                    mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y, y.x, y.y, y.x, y.y);
+                                } else {
+                                    mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y);
                                 }
                             }
-#pragma unroll
-                            for (int pc = 0; pc < 2 * QP - 1; ++pc) {
-                                const uint32_t b0 = pack_bf2(a[0], a[1]), b1 = pack_bf2(a[2], a[3]);
-                                a[0] -= bf_lo(b0); a[1] -= bf_hi(b0); a[2] -= bf_lo(b1); a[3] -= bf_hi(b1);
-                                mma_bf16(sc[0][nt], kw[0][2 * x], kw[1][2 * x], kw[0][2 * x + 1], kw[1][2 * x + 1], b0, b1);
-                                mma_bf16(sc[1][nt], kw[2][2 * x], kw[3][2 * x], kw[2][2 * x + 1], kw[3][2 * x + 1], b0, b1);
-                            }
                         }
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {     // sums below 2^22: the low bits of 1.5 * 2^23 + sum
+                            const float x0 = __int_as_float(acc[0][mt][nt][e]) - 12582912.f;
+                            const float x1 = __int_as_float(acc[1][mt][nt][e]) - 12582912.f;
+                            const float x2 = __int_as_float(acc[2][mt][nt][e]) - 12582912.f;
+                            sc[mt][nt][e] = fmaf(x0, 65536.f, fmaf(x1, 256.f, x2));
+                        }
+            } else {
+                // 16 tokens of the open block in bf16; q put together again and split into bf16 pieces, which
+                // three hold. Rows behind the last token hold anything and count as zeros.
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+#pragma unroll 1
+                for (int y = 0; y < D / 16; ++y) {        // 4 channels e0 .. + 3
+                    const int e0 = 16 * y + 4 * tq;
+                    uint2 k0 = make_uint2(0u, 0u), k1 = k0;
+                    if (gq < left && e0 < c.d) k0 = *reinterpret_cast<const uint2*>(kp + (gq * c.d + e0) * 2);
+                    if (gq + 8 < left && e0 < c.d) k1 = *reinterpret_cast<const uint2*>(kp + ((gq + 8) * c.d + e0) * 2);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int z = 0; z < 3; ++z) {
+                            const uint32_t word = reinterpret_cast<const uint32_t*>(s_q)[(((nt * 3 + z) * (D / 32) + (y >> 1)) * 32 + lane) * 2 + (y & 1)];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) a[j] = fmaf(a[j], 256.f, (float)(int8_t)(word >> (8 * j)));
+                        }
+#pragma unroll
+                        for (int pc = 0; pc < 3; ++pc) {
+                            const uint32_t b0 = pack_bf2(a[0], a[1]), b1 = pack_bf2(a[2], a[3]);
+                            a[0] -= bf_lo(b0); a[1] -= bf_hi(b0); a[2] -= bf_lo(b1); a[3] -= bf_hi(b1);
+                            mma_bf16(sc[0][nt], k0.x, k1.x, k0.y, k1.y, b0, b1);
+                        }
+                    }
                 }
             }
             // logits, running maximum, weights
-            const int left = what == -1 ? 0 : what == -2 ? r : 32;          // tokens of this unit
-            const bool masked = left < 32 || 32 * b + 31 > all_see;
-            float ga[NT][2], gb[NT][2];
+            const bool masked = left < 32 || pos0 + 31 > all_see;
+            auto gone = [&](int nt, int e, int t) { return gq + 8 * t >= left || pos0 + gq + 8 * t > sees[nt][e]; };
+            float ga[NT][2], gb[NT][2], top[NT][2];
             bool grown = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -446,39 +549,42 @@ __global__ void __launch_bounds__(Ring<D>::warps * 32, 1) k_b8_attn(const __grid
                 for (int e = 0; e < 2; ++e) {
                     ga[nt][e] = fh[nt][e] * ks;
                     gb[nt][e] = fmaf(fh[nt][e], ks, -ga[nt][e]) + fl[nt][e] * ks;
-                    float top = -INFINITY;
+                    float y[4];                                              // of token gq + 8 t
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {                            // token gq + 8 t
-                        const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
-                        float y = fmaf(raw, ga[nt][e], raw * gb[nt][e]);
-                        if (masked && (gq + 8 * t >= left || 32 * b + gq + 8 * t > last[nt][e])) y = -INFINITY;
-                        top = fmaxf(top, y);
-                        if (lg && row0 + 8 * nt + 2 * tq + e < rows)
-                            lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] = y;
+                    for (int t = 0; t < 4; ++t) y[t] = sc[t >> 1][nt][2 * (t & 1) + e] * ga[nt][e];
+                    if (masked) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (gone(nt, e, t)) y[t] = -INFINITY;
                     }
-                    grown = grown || top > m[nt][e] + kSlack;
+                    top[nt][e] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    grown = grown || top[nt][e] > m[nt][e] + kSlack;
                 }
-            if (what == -1) {
-                stage_in(i + ST);
-                continue;
+            if (WT) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (row0 + 8 * nt + 2 * tq + e < rows)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                if (what >= 0 || t < 2) {
+                                    const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
+                                    lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] =
+                                        masked && gone(nt, e, t) ? -INFINITY : fmaf(raw, ga[nt][e], raw * gb[nt][e]);
+                                }
             }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = m[nt][e];
+                        float t = fmaxf(m[nt][e], top[nt][e]);
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
-                            float y = fmaf(raw, ga[nt][e], raw * gb[nt][e]);
-                            if (masked && (gq + 8 * t >= left || 32 * b + gq + 8 * t > last[nt][e])) y = -INFINITY;
-                            top = fmaxf(top, y);
-                        }
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float f = m[nt][e] == -INFINITY ? 0.f : tq_exp2(m[nt][e] - top);
-                        m[nt][e] = top;
+                        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                        const float f = m[nt][e] == -INFINITY ? 0.f : tq_exp2(m[nt][e] - t);
+                        m[nt][e] = t;
+                        big = big || (fabsf(t) >= 65536.f && t != -INFINITY);
                         l[nt][e] *= f;
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
@@ -486,29 +592,52 @@ __global__ void __launch_bounds__(Ring<D>::warps * 32, 1) k_b8_attn(const __grid
                             o[mt][nt][2 + e] *= f;
                         }
                     }
+                big = __any_sync(0xffffffffu, big);
             }
-            // Beyond 2^16 m itself is rounded by more than a weight could show: subtract the rounded logits
-            // there, of which the largest is m exactly.
-            bool big = false;
+            if (big) {
+                // Beyond 2^16 m itself is rounded by more than a weight could show: subtract the rounded logits,
+                // of which the largest is m exactly.
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) big = big || fabsf(m[nt][0]) >= 65536.f || fabsf(m[nt][1]) >= 65536.f;
-            big = __any_sync(0xffffffffu, big);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
+                            const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                            x = __fadd_rn(__fsub_rn(__fmul_rn(x, ga[nt][e]), mm), kBias);
+                        }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
+                            const float ref = kBias - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]);
+                            x = fmaf(x, ga[nt][e], fmaf(x, gb[nt][e], ref));
+                        }
+            }
+            if (masked) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (gone(nt, e, t)) sc[t >> 1][nt][2 * (t & 1) + e] = -INFINITY;
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                        const float small = x * gb[nt][e];
-                        float pr = tq_exp2(big ? __fadd_rn(__fsub_rn(fmaf(x, ga[nt][e], small), mm), kBias)
-                                               : fmaf(x, ga[nt][e], small + (kBias - mm)));
-                        if (masked && (gq + 8 * t >= left || 32 * b + gq + 8 * t > last[nt][e])) pr = 0.f;
-                        x = pr;
-                        l[nt][e] += pr;
+                        x = tq_exp2(x);
+                        l[nt][e] += x;
                     }
-                }
             if (what >= 0) {
                 uint32_t pf[2][NT][2][2];                 // P^T as B fragments: [token half][n-tile][piece][register]
 #pragma unroll
@@ -523,276 +652,285 @@ __global__ void __launch_bounds__(Ring<D>::warps * 32, 1) k_b8_attn(const __grid
                             pf[y][nt][0][e] = transpose8(hi);
                             pf[y][nt][1][e] = transpose8(pack_h2(a - t.x, b2 - t.y));
                         }
-                uint32_t vw[8][VW];                       // tokens 16 y + 2 tq, + 1, + 8, + 9
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const int tok = 16 * (t >> 2) + 2 * tq + (t & 1) + 8 * (t >> 1 & 1);
-                    const uint8_t* row = vp + tok * D;
-                    if (D == 64) {
-                        const uint2 a = *reinterpret_cast<const uint2*>(row + (((gq >> 1) ^ b8_swz(tok, D / 16)) << 4) + (gq & 1) * 8);
+                for (int z = 0; z < VW / 2; ++z) {        // 8 channels of a lane at a time
+                    uint32_t vw[8][2];                    // tokens 16 y + 2 tq, + 1, + 8, + 9
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const uint2 a = *reinterpret_cast<const uint2*>(
+                            kp + (t & 1 ? at_v1 : at_v0) + (16 * (t >> 2) + 8 * (t >> 1 & 1)) * D + (z & 1) * 8 + (z >> 1) * 128);
                         vw[t][0] = a.x; vw[t][1] = a.y;
-                    } else {
+                    }
 #pragma unroll
-                        for (int y = 0; y < VW / 4; ++y) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(row + (((gq + 8 * y) ^ b8_swz(tok, D / 16)) << 4));
-                            vw[t][4 * y] = a.x; vw[t][4 * y + 1] = a.y; vw[t][4 * y + 2] = a.z; vw[t][4 * y + 3] = a.w;
+                    for (int x = 0; x < 2; ++x) {
+                        float acc[2][NT][4];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t v0 = vw[4 * y][x], v1 = vw[4 * y + 1][x], v8 = vw[4 * y + 2][x], v9 = vw[4 * y + 3][x];
+                            const uint32_t l0 = __byte_perm(v0, v1, 0x5140), h0 = __byte_perm(v0, v1, 0x7362);
+                            const uint32_t l8 = __byte_perm(v8, v9, 0x5140), h8 = __byte_perm(v8, v9, 0x7362);
+                            const uint32_t a0 = codes_h2<0x4140>(l0), a1 = codes_h2<0x4342>(l0), a2 = codes_h2<0x4140>(l8),
+                                           a3 = codes_h2<0x4342>(l8);
+                            const uint32_t b0 = codes_h2<0x4140>(h0), b1 = codes_h2<0x4342>(h0), b2 = codes_h2<0x4140>(h8),
+                                           b3 = codes_h2<0x4342>(h8);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int pc = 0; pc < 2; ++pc) {
+                                    const uint32_t p0 = pf[y][nt][pc][0], p1 = pf[y][nt][pc][1];
+                                    if (y == 0 && pc == 0) {
+                                        mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1, 0.f, 0.f, 0.f, 0.f);
+                                        mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1, 0.f, 0.f, 0.f, 0.f);
+                                    } else {
+                                        mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1);
+                                        mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1);
+                                    }
+                                }
                         }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float& y = o[2 * (2 * z + x) + j][nt][e];
+                                    y = fmaf(vs, acc[j][nt][e], y);
+                                }
                     }
-                }
-#pragma unroll
-                for (int x = 0; x < VW; ++x) {
-                    float acc[2][NT][4];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t v0 = vw[4 * y][x], v1 = vw[4 * y + 1][x], v8 = vw[4 * y + 2][x], v9 = vw[4 * y + 3][x];
-                        const uint32_t l0 = __byte_perm(v0, v1, 0x5140), h0 = __byte_perm(v0, v1, 0x7362);
-                        const uint32_t l8 = __byte_perm(v8, v9, 0x5140), h8 = __byte_perm(v8, v9, 0x7362);
-                        const uint32_t a0 = codes_h2<0x4140>(l0), a1 = codes_h2<0x4342>(l0), a2 = codes_h2<0x4140>(l8),
-                                       a3 = codes_h2<0x4342>(l8);
-                        const uint32_t b0 = codes_h2<0x4140>(h0), b1 = codes_h2<0x4342>(h0), b2 = codes_h2<0x4140>(h8),
-                                       b3 = codes_h2<0x4342>(h8);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int pc = 0; pc < 2; ++pc) {
-                                tq_hmma(acc[0][nt], a0, a1, a2, a3, pf[y][nt][pc][0], pf[y][nt][pc][1]);
-                                tq_hmma(acc[1][nt], b0, b1, b2, b3, pf[y][nt][pc][0], pf[y][nt][pc][1]);
-                            }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[2 * x + j][nt][e] = fmaf(vs, acc[j][nt][e], o[2 * x + j][nt][e]);
                 }
             } else {
                 // open block: bf16 values, three bf16 pieces of the weights. A value that is not finite must
                 // not meet the zero weight of a row that does not see its token: then token by token.
-                const uint16_t* vg = b8_open(c, s, h, 1);
                 bool wild = false;
-                for (int t = lane; t < r * c.d / 8; t += 32) {
-                    const uint4 a = reinterpret_cast<const uint4*>(vg)[t];
+                for (int t = lane; t < left * c.d / 8; t += 32) {
+                    const uint4 a = reinterpret_cast<const uint4*>(vp)[t];
                     const uint32_t u4[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         wild = wild || (u4[y] & 0x7f80u) == 0x7f80u || (u4[y] & 0x7f800000u) == 0x7f800000u;
                 }
                 if (!__any_sync(0xffffffffu, wild)) {
-                    uint32_t pf[2][NT][3][2];
+                    uint32_t pf[NT][3][2];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int e = 0; e < 2; ++e) {
+                            float a = sc[0][nt][2 * e], b2 = sc[0][nt][2 * e + 1];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float a = sc[y][nt][2 * e], b2 = sc[y][nt][2 * e + 1];
-#pragma unroll
-                                for (int pc = 0; pc < 3; ++pc) {
-                                    const uint32_t t = pack_bf2(a, b2);
-                                    a -= bf_lo(t);
-                                    b2 -= bf_hi(t);
-                                    pf[y][nt][pc][e] = transpose8(t);
-                                }
+                            for (int pc = 0; pc < 3; ++pc) {
+                                const uint32_t t = pack_bf2(a, b2);
+                                a -= bf_lo(t);
+                                b2 -= bf_hi(t);
+                                pf[nt][pc][e] = transpose8(t);
                             }
+                        }
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {            // 8 channels D / 8 gq + 8 x
-                        uint32_t vw[8][4];
-                        const int e0 = gq * (D / 8) + 8 * x;
+                    for (int x = 0; x < D / 64; ++x) {            // 8 channels of a lane: m-tiles 4 x .. 4 x + 3
+                        uint32_t vw[4][4];
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            const int tok = 16 * (t >> 2) + 2 * tq + (t & 1) + 8 * (t >> 1 & 1);
+                        for (int t = 0; t < 4; ++t) {
+                            const int tok = 2 * tq + (t & 1) + 8 * (t >> 1), ch = channel<D>(gq, 4 * x, 0);
                             uint4 a = make_uint4(0u, 0u, 0u, 0u);
-                            const int ch = D == 256 ? 16 * (gq + 8 * (x >> 1)) + 8 * (x & 1) : e0;
-                            if (tok < r && ch < c.d) a = *reinterpret_cast<const uint4*>(vg + tok * c.d + ch);
+                            if (tok < left && ch < c.d) a = *reinterpret_cast<const uint4*>(vp + (tok * c.d + ch) * 2);
                             vw[t][0] = a.x; vw[t][1] = a.y; vw[t][2] = a.z; vw[t][3] = a.w;
                         }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)               // m-tile 4 x + j: channels + 2 j, + 2 j + 1
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5410), a1 = __byte_perm(vw[0][j], vw[1][j], 0x7632);
+                            const uint32_t a2 = __byte_perm(vw[2][j], vw[3][j], 0x5410), a3 = __byte_perm(vw[2][j], vw[3][j], 0x7632);
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t v0 = vw[4 * y][j], v1 = vw[4 * y + 1][j], v8 = vw[4 * y + 2][j],
-                                               v9 = vw[4 * y + 3][j];
-                                const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
-                                const uint32_t a2 = __byte_perm(v8, v9, 0x5410), a3 = __byte_perm(v8, v9, 0x7632);
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int pc = 0; pc < 3; ++pc)
-                                        mma_bf16(o[4 * x + j][nt], a0, a1, a2, a3, pf[y][nt][pc][0], pf[y][nt][pc][1]);
-                            }
+                                for (int pc = 0; pc < 3; ++pc)
+                                    mma_bf16(o[4 * x + j][nt], a0, a1, a2, a3, pf[nt][pc][0], pf[nt][pc][1]);
+                        }
                     }
                 } else {
-                    for (int t = 0; t < r; ++t)
+#pragma unroll 1
+                    for (int t = 0; t < left; ++t)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int src = (t & 7) * 4 + tq;
-                                const float x0 = __shfl_sync(0xffffffffu, sc[0][nt][e], src);
-                                const float x1 = __shfl_sync(0xffffffffu, sc[0][nt][2 + e], src);
-                                const float x2 = __shfl_sync(0xffffffffu, sc[1][nt][e], src);
-                                const float x3 = __shfl_sync(0xffffffffu, sc[1][nt][2 + e], src);
-                                const float pr = t < 8 ? x0 : t < 16 ? x1 : t < 24 ? x2 : x3;
+                                const float y0 = __shfl_sync(0xffffffffu, sc[0][nt][e], (t & 7) * 4 + tq);
+                                const float y1 = __shfl_sync(0xffffffffu, sc[0][nt][2 + e], (t & 7) * 4 + tq);
+                                const float pr = t < 8 ? y0 : y1;
                                 if (pr == 0.f) continue;
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                    for (int y = 0; y < 2; ++y) {
-                                        const int ch = D == 256 ? 16 * (gq + 8 * (mt >> 3)) + 2 * (mt & 7) + y
-                                                                : gq * (D / 8) + 2 * mt + y;
-                                        if (ch < c.d)
-                                            o[mt][nt][2 * y + e] =
-                                                fmaf(pr, __uint_as_float((uint32_t)vg[t * c.d + ch] << 16), o[mt][nt][2 * y + e]);
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    const int ch = channel<D>(gq, mt, 0);
+                                    if (ch < c.d) {
+                                        const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vp + (t * c.d + ch) * 2);
+                                        o[mt][nt][e] = fmaf(pr, bf_lo(v2), o[mt][nt][e]);
+                                        o[mt][nt][2 + e] = fmaf(pr, bf_hi(v2), o[mt][nt][2 + e]);
                                     }
+                                }
                             }
                 }
             }
+            }
             __syncwarp();                                 // every lane has read the stage
-            stage_in(i + ST);
+            issue(i + ST, st);
+            st += NW;
+            if (st >= ST) {
+                st -= ST;
+                phase ^= 1u;
+            }
         }
 
-        // the warps' sums meet: one maximum per row, then a sum over the warps in order
+        // the warps' sums meet: one maximum per row, then a sum over the warps in a fixed order
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-                if (gq == 0) {
-                    s_m[w][8 * nt + 2 * tq + e] = m[nt][e];
-                    s_l[w][8 * nt + 2 * tq + e] = l[nt][e];
-                }
+                if (gq == 0) s_ml[8 * nt + 2 * tq + e][w] = make_float2(m[nt][e], l[nt][e]);
             }
         __syncthreads();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + 2 * tq + e;
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < NW; ++x) top = fmaxf(top, s_m[x][r]);
-                const float f = m[nt][e] == -INFINITY ? (l[nt][e] == 0.f ? 0.f : NAN) : tq_exp2(m[nt][e] - top);
-                float* dst = s_o + (size_t)(w * 8 * NT + r) * D;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int ch = D == 256 ? 16 * (gq + 8 * (mt >> 3)) + 2 * (mt & 7) + y : gq * (D / 8) + 2 * mt + y;
-                        dst[ch] = f == 0.f ? 0.f : o[mt][nt][2 * y + e] * f;
-                    }
+        for (int r = w; r < 8 * NT; r += NW) {
+            const float2 ml = lane < NW ? s_ml[r][lane] : make_float2(-INFINITY, 0.f);
+            const float top = tq_warp_max(ml.x), sum = tq_warp_sum(ml.x == -INFINITY ? ml.y : ml.y * tq_exp2(ml.x - top));
+            if (lane < NW) s_fac[r][lane] = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : tq_exp2(ml.x - top);
+            if (lane == 0) {
+                s_top[r] = top;
+                s_sum[r] = sum;
             }
-        __syncthreads();
+        }
         const bool whole = part == units;
-        const int slot = 2 * blockIdx.x + (off == 0 ? 1 : 0);
-        for (int t = threadIdx.x; t < 8 * NT * (D / 4); t += NW * 32) {
-            const int r = t / (D / 4), e = t % (D / 4) * 4;
-            if (row0 + r >= rows) continue;
-            float top = -INFINITY, sum = 0.f;
+        const size_t slot = 2 * (size_t)blockIdx.x + (off == 0 ? 1 : 0);
+        constexpr int LC = 2 * MT / RD, RS = 8 * LC + 4;  // channels of a lane per round; a row's pitch
+        constexpr int G = NW == 16 ? 4 : NW == 12 ? 2 : 1, items = 8 * NT * 2 * LC;
+        static_assert(items * G <= NW * 32, "one pass");
 #pragma unroll
-            for (int x = 0; x < NW; ++x) top = fmaxf(top, s_m[x][r]);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int rd = 0; rd < RD; ++rd) {
+            if (rd) __syncthreads();
 #pragma unroll
-            for (int x = 0; x < NW; ++x) {
-                const float4 y = *reinterpret_cast<const float4*>(s_o + (size_t)(x * 8 * NT + r) * D + e);
-                a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
-                const float mx = s_m[x][r];
-                sum += mx == -INFINITY ? s_l[x][r] : s_l[x][r] * tq_exp2(mx - top);
-            }
-            if (whole) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                if (e < c.d)
-                    *reinterpret_cast<float4*>(p.out + q_row(row0 + r) * c.d + e) =
-                        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                if (e == 0 && p.acc_out)
-                    p.lse[(s * c.n_kv + h) * (int64_t)(p.n_q * p.g) + row0 + r] =
-                        sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
-            } else {
-                *reinterpret_cast<float4*>(p.part + ((size_t)slot * 8 * NT + r) * D + e) = a;
-                if (e == 0) {
-                    p.part_ml[((size_t)slot * 8 * NT + r) * 2] = top;
-                    p.part_ml[((size_t)slot * 8 * NT + r) * 2 + 1] = sum;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (row0 + 8 * nt + 2 * tq + e >= rows) continue;
+                    float* dst = s_o + (size_t)(w * 8 * NT + 8 * nt + 2 * tq + e) * RS + gq * LC;
+#pragma unroll
+                    for (int k = 0; k < LC / 4; ++k) {
+                        const int mt = rd * (MT / RD) + 2 * k;
+                        *reinterpret_cast<float4*>(dst + 4 * k) =
+                            make_float4(o[mt][nt][e], o[mt][nt][2 + e], o[mt + 1][nt][e], o[mt + 1][nt][2 + e]);
+                    }
+                }
+            __syncthreads();
+            const int t = threadIdx.x / G, xg = threadIdx.x % G, r = t / (2 * LC), cg = t % (2 * LC) / (LC / 4), c4 = t % (LC / 4) * 4;
+            if (t < items && row0 + r < rows) {           // (the G threads of an item are neighbours in a warp)
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < NW / G; ++y) {
+                    const int x = xg * (NW / G) + y;
+                    const float f = s_fac[r][x];
+                    const float4 z = *reinterpret_cast<const float4*>(s_o + (size_t)(x * 8 * NT + r) * RS + cg * LC + c4);
+                    if (f != 0.f) {
+                        a.x = fmaf(z.x, f, a.x); a.y = fmaf(z.y, f, a.y); a.z = fmaf(z.z, f, a.z); a.w = fmaf(z.w, f, a.w);
+                    }
+                }
+                const uint32_t team = __activemask();
+#pragma unroll
+                for (int d = 1; d < G; d <<= 1) {
+                    a.x += __shfl_xor_sync(team, a.x, d); a.y += __shfl_xor_sync(team, a.y, d);
+                    a.z += __shfl_xor_sync(team, a.z, d); a.w += __shfl_xor_sync(team, a.w, d);
+                }
+                const int ch = channel<D>(cg, rd * (MT / RD) + c4 / 2, 0);
+                if (xg == 0) {
+                    if (whole) {
+                        const float sum = s_sum[r], inv = sum == 0.f ? 0.f : 1.f / sum;
+                        if (ch < c.d)
+                            *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r) * c.d + ch) =
+                                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                    } else {
+                        *reinterpret_cast<float4*>(p.part + (slot * 8 * NT + r) * D + ch) = a;
+                    }
                 }
             }
         }
-        __syncthreads();                                  // s_m and s_o are free again
+        float* lse = p.lse + ((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0;
+        if (threadIdx.x < 8 * NT && row0 + threadIdx.x < rows) {
+            const float top = s_top[threadIdx.x], sum = s_sum[threadIdx.x];
+            if (!whole)
+                *reinterpret_cast<float2*>(p.part_ml + (slot * 8 * NT + threadIdx.x) * 2) = make_float2(top, sum);
+            else if (WT)
+                lse[threadIdx.x] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+        }
+        __syncthreads();                                  // s_o and the row sums are free again
+        if (!whole) {
+            // The CTA that brings a segment's last part joins all of them, in their order. The count of a
+            // segment that begins in CTA c0 and goes on is byte c0 of the workspace's counters, back at 0 after.
+            const int first = pl.u0 + u - off;
+            const int c0 = pl.c0 >= 0 ? pl.c0 : pl.owner(first), c1 = pl.c0 >= 0 ? pl.c1 : pl.owner(first + units - 1);
+            if (threadIdx.x == 0) {
+                const uint32_t sh = 8 * (c0 & 3);
+                const uint32_t got = (atomic_add_acq_rel(p.count + (c0 >> 2), 1u << sh) >> sh & 255u) + 1;
+                s_last = (int)got == c1 - c0 + 1;
+                if (s_last) atomicSub(p.count + (c0 >> 2), got << sh);
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                float2* fac = reinterpret_cast<float2*>(s_o);   // [part][row]: maximum and sum, then the factor
+                for (int r = w; r < 8 * NT && row0 + r < rows; r += NW) {
+                    float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+                    for (int x = c0 + lane; x <= c1; x += 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * 2));
+                        fac[(x - c0) * 8 * NT + r] = ml;
+                        top = fmaxf(top, ml.x);
+                    }
+                    top = tq_warp_max(top);
+#pragma unroll 1
+                    for (int x = c0 + lane; x <= c1; x += 32) {
+                        const float2 ml = fac[(x - c0) * 8 * NT + r];
+                        const float y = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : tq_exp2(ml.x - top);
+                        fac[(x - c0) * 8 * NT + r].x = y;
+                        sum = y == 0.f ? sum : fmaf(ml.y, y, sum);
+                    }
+                    sum = tq_warp_sum(sum);
+                    if (lane == 0) {
+                        s_sum[r] = sum;
+                        if (WT) lse[r] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+                    }
+                }
+                __syncthreads();
+#pragma unroll 1
+                for (int t = threadIdx.x; t < 8 * NT * D; t += NW * 32) {      // 4 threads per (row, 4 channels)
+                    const int r = t / D, e = t % D / 4 * 4;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (row0 + r < rows) {
+#pragma unroll 4
+                        for (int x = c0 + (t & 3); x <= c1; x += 4) {
+                            const float y = fac[(x - c0) * 8 * NT + r].x;
+                            const float4 z = __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * D + e));
+                            a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 1; d < 4; d <<= 1) {
+                        a.x += __shfl_xor_sync(0xffffffffu, a.x, d); a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
+                        a.z += __shfl_xor_sync(0xffffffffu, a.z, d); a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+                    }
+                    if ((t & 3) == 0 && row0 + r < rows && e < c.d) {
+                        const float inv = s_sum[r] == 0.f ? 0.f : 1.f / s_sum[r];
+                        *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r) * c.d + e) =
+                            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                    }
+                }
+                __syncthreads();
+            }
+        }
         u += part;
         x0 += part;
     }
-    if (!ok) {
-        // a copy did not land in time: record it and give those in flight a bounded time
-        if (lane == 0) {
-            tq_raise(c.status, TQ_FLAG_TIMEOUT);
-            for (int st = 0; st < ST; ++st)
-                if (in_flight >> st & 1u) tq_mbar_wait(&s_full[w * ST + st], phase >> st & 1u, kWaitLimit);
-        }
-    }
-}
-
-// Joins the parts of a segment that several CTAs shared, in their order; rows of sequences without
-// any token are zeros. One CTA per segment.
-constexpr int kMergeThreads = 256;
-template <int D, int NT>
-__global__ void __launch_bounds__(kMergeThreads) k_b8_merge(const __grid_constant__ B8AttnParams p) {
-    __shared__ int64_t s_scan[kMergeThreads / 32];
-    const B8Cache& c = p.c;
-    const int segs = c.n_kv * p.row_tiles;
-    const int64_t v = blockIdx.x / segs;
-    const int seg = (int)(blockIdx.x - v * segs), h = seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * 8 * NT;
-    Plan pl;
-    plan_total<kMergeThreads>(p, pl, s_scan);
-    int64_t before = 0;
-    for (int64_t v0 = 0; v0 <= v; v0 += kMergeThreads) {
-        const int64_t x = v0 + threadIdx.x;
-        int n;
-        int64_t sum;
-        block_scan<kMergeThreads>(x < v ? (int64_t)virt_units(p, x, n) * segs : 0, s_scan, sum);
-        before += sum;
-    }
-    int n;
-    const int units = virt_units(p, v, n);
-    const int64_t s = p.sel ? v / p.n_q : v;
-    const int first_q = p.sel ? (int)(v - s * p.n_q) : 0;
-    const int rows = p.sel ? p.g : p.n_q * p.g;
-    const int64_t qbase = (s * p.n_q + first_q) * c.n_kv * p.g + (int64_t)h * p.g;
-    const int64_t a0 = before + (int64_t)seg * units, a1 = a0 + units;
-    const int c0 = units ? owner(pl, a0) : 0, c1 = units ? owner(pl, a1 - 1) : 0;
-    tq_pdl_wait();
-    if (units && c0 == c1) return;                        // finished where it was computed
-    for (int t = threadIdx.x; t < 8 * NT * (D / 4); t += kMergeThreads) {
-        const int r = t / (D / 4), e = t % (D / 4) * 4;
-        if (row0 + r >= rows) continue;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float top = -INFINITY, sum = 0.f;
-        if (units) {
-            for (int x = c0; x <= c1; ++x) {
-                const int slot = 2 * x + (share(pl, x) <= a0 ? 1 : 0);
-                top = fmaxf(top, p.part_ml[((size_t)slot * 8 * NT + r) * 2]);
-            }
-            for (int x = c0; x <= c1; ++x) {
-                const int slot = 2 * x + (share(pl, x) <= a0 ? 1 : 0);
-                const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot * 8 * NT + r) * 2);
-                const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : tq_exp2(ml.x - top);
-                if (f == 0.f) continue;
-                const float4 y = *reinterpret_cast<const float4*>(p.part + ((size_t)slot * 8 * NT + r) * D + e);
-                a.x = fmaf(y.x, f, a.x); a.y = fmaf(y.y, f, a.y); a.z = fmaf(y.z, f, a.z); a.w = fmaf(y.w, f, a.w);
-                sum = fmaf(ml.y, f, sum);
-            }
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t row = qbase + (int64_t)((row0 + r) / p.g) * c.n_kv * p.g + (row0 + r) % p.g;
-        if (e < c.d)
-            *reinterpret_cast<float4*>(p.out + row * c.d + e) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        if (e == 0 && p.acc_out)
-            p.lse[(s * c.n_kv + h) * (int64_t)(p.n_q * p.g) + row0 + r] =
-                sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+    if (!ok && lane == 0) {
+        // a copy did not land in time: record it and give those that may be in flight a bounded time
+        tq_raise(c.status, TQ_FLAG_TIMEOUT);
+        for (int k = max(w, i - NW * (early + 1)); k < min(i, mine); k += NW)
+            tq_mbar_wait(&s_full[k % ST], (uint32_t)(k / ST) & 1u, kWaitLimit);
     }
 }
 
@@ -831,33 +969,38 @@ __global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8At
     p.acc_out[at] = a;
 }
 
-template <int D, int NT, int QP>
-cudaError_t launch(const B8AttnParams& p, cudaStream_t st) {
+template <int D, int NT, bool WT>
+cudaError_t launch_one(const B8AttnParams& p, cudaStream_t st) {
+    using Sh = Shape<D, NT>;
     static TqLaunchCache cache;
-    cudaError_t e = tq_kernel_setup(k_b8_attn<D, NT, QP>, Ring<D>::warps * 32, smem_bytes<D, NT>(), cache, nullptr, nullptr);
+    const cudaError_t e = tq_kernel_setup(k_b8_attn<D, NT, WT>, Sh::warps * 32, Sh::smem, cache, nullptr, nullptr);
     if (e != cudaSuccess) return e;
-    k_b8_attn<D, NT, QP><<<(unsigned)p.grid, Ring<D>::warps * 32, smem_bytes<D, NT>(), st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t segs = (p.sel ? p.c.n_seq * p.n_q : p.c.n_seq) * p.c.n_kv * p.row_tiles;
-    if (segs > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return tq_launch_pdl(k_b8_merge<D, NT>, dim3((unsigned)segs), dim3(kMergeThreads), 0, st, p);
+    k_b8_attn<D, NT, WT><<<(unsigned)p.grid, Sh::warps * 32, Sh::smem, st>>>(p);
+    return cudaGetLastError();
+}
+template <int D, int NT>
+cudaError_t launch(const B8AttnParams& p, cudaStream_t st) {
+    return p.acc_out ? launch_one<D, NT, true>(p, st) : launch_one<D, NT, false>(p, st);
 }
 
 }  // namespace
 
 int b8_attn_row_tile(int D, int rows) { return rows <= 8 || D == 256 ? 8 : 16; }
-int b8_attn_grid() { return tq_device_sms(); }
+int b8_attn_grid() { return tq_device_sms() < kB8Counters ? tq_device_sms() : kB8Counters; }
 
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     const int64_t virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
     const int64_t tiles = (p.c.max_blocks * 32 + kAccTok - 1) / kAccTok;
-    if (virt * p.c.n_kv * p.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // the kernel counts units in 31 bits
+    const int64_t most = (p.sel ? p.n_sel : p.c.max_blocks) + 1;
+    if (virt * p.c.n_kv * p.row_tiles > 0x3fffffffLL || most * (virt * p.c.n_kv * p.row_tiles) > 0x3fffffffLL)
+        return cudaErrorInvalidValue;
     if (p.acc_out && tiles * p.c.n_seq * p.c.n_kv > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const bool wide = p.row_tile == 16, f32 = p.q_dtype == 0;
+    const bool wide = p.row_tile == 16;
     cudaError_t e;
-    if (p.c.D == 64) e = wide ? (f32 ? launch<64, 2, 2>(p, st) : launch<64, 2, 1>(p, st)) : (f32 ? launch<64, 1, 2>(p, st) : launch<64, 1, 1>(p, st));
-    else if (p.c.D == 128) e = wide ? (f32 ? launch<128, 2, 2>(p, st) : launch<128, 2, 1>(p, st)) : (f32 ? launch<128, 1, 2>(p, st) : launch<128, 1, 1>(p, st));
-    else e = f32 ? launch<256, 1, 2>(p, st) : launch<256, 1, 1>(p, st);
+    if (p.c.D == 64) e = wide ? launch<64, 2>(p, st) : launch<64, 1>(p, st);
+    else if (p.c.D == 128) e = wide ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
+    else e = launch<256, 1>(p, st);
     if (e != cudaSuccess || !p.acc_out) return e;
     k_b8_acc<<<(unsigned)(tiles * p.c.n_seq * p.c.n_kv), kAccTok, 0, st>>>(p, tiles);
     return cudaGetLastError();

@@ -279,7 +279,7 @@ size_t tq_workspace_bytes(const tq_codec* c, int op, int64_t a, int64_t b, int64
 
 int tq_reset_status(void* ws, void* stream) {
     if (!ws) return TQ_ERR_ARG;
-    return cuda_status(cudaMemsetAsync(ws, 0, 4, static_cast<cudaStream_t>(stream)));
+    return cuda_status(cudaMemsetAsync(ws, 0, TQ_STATUS_BYTES, static_cast<cudaStream_t>(stream)));
 }
 
 int tq_get_status(void* ws, void* stream) {

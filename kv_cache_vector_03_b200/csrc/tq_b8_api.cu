@@ -11,6 +11,7 @@
 
 namespace {
 
+static_assert(64 + kB8Counters <= TQ_STATUS_BYTES, "the arrival counts share the status word's bytes");
 constexpr int64_t kMaxBlocks = (int64_t)1 << 25;
 
 size_t align_up(size_t v) { return (v + TQ_ALIGN - 1) / TQ_ALIGN * TQ_ALIGN; }
@@ -162,6 +163,7 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     p.logit_row = W.logit_row;
     p.part = reinterpret_cast<float*>(wsb + W.part);
     p.part_ml = reinterpret_cast<float*>(wsb + W.ml);
+    p.count = reinterpret_cast<uint32_t*>(wsb) + 16;
     p.grid = b8_attn_grid();
     p.row_tile = b8_attn_row_tile(p.c.D, sel ? g : n_q * g);
     p.row_tiles = ((sel ? g : n_q * g) + p.row_tile - 1) / p.row_tile;

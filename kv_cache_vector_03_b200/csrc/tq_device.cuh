@@ -210,6 +210,23 @@ TQ_DEVICE void tq_bulk_load(void* dst_smem, const void* src, uint32_t bytes, uin
         : "memory");
 }
 
+// two copies that complete one phase together
+TQ_DEVICE void tq_bulk_load2(void* dst_a, const void* a, uint32_t a_bytes, void* dst_b, const void* b,
+                             uint32_t b_bytes, uint64_t* bar) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(tq_smem_addr(bar)), "r"(a_bytes + b_bytes)
+                 : "memory");
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+            tq_smem_addr(dst_a)),
+        "l"(a), "r"(a_bytes), "r"(tq_smem_addr(bar))
+        : "memory");
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+            tq_smem_addr(dst_b)),
+        "l"(b), "r"(b_bytes), "r"(tq_smem_addr(bar))
+        : "memory");
+}
+
 TQ_DEVICE bool tq_mbar_wait(uint64_t* bar, uint32_t phase, uint32_t limit) {
     const uint32_t a = tq_smem_addr(bar);
     for (uint32_t it = 0; it < limit; ++it) {
