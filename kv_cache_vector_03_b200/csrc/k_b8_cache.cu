@@ -157,50 +157,84 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
     }
 }
 
-// one warp per (sequence, token, keys or values); a lane takes 8 channels of a head at a time
+// One warp per (sequence, 4 tokens of one block, keys or values): a lane takes 16 channels of a head of all four
+// tokens at a time, so four 16-byte loads are under way, and writes 32 or 64 bytes of each.
 template <int D, bool F32>
-__global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p) {
+__global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p, int64_t groups) {
     const B8Cache& c = p.c;
     const int lane = threadIdx.x & 31;
     int64_t id = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
     const int side = (int)(id & 1);
     id >>= 1;
-    const int64_t s = id / p.n_tok, j = id - s * p.n_tok;
+    const int64_t s = id / groups;
     if (s >= c.n_seq) return;
     const int n = b8_len(c, s);
-    const int64_t pos = n - p.n_tok + j;
-    if (pos < 0) return;
-    const int b = (int)(pos >> 5), t = (int)(pos & 31), chunks = c.d / 8;
+    const int64_t from = max((int64_t)0, n - p.n_tok);
+    const int64_t pos = (from & ~(int64_t)3) + 4 * (id - s * groups);   // its tokens: pos .. pos + 3, from `from` to n
+    if (pos >= n) return;
+    const int b = (int)(pos >> 5), t0 = (int)(pos & 31), chunks = (c.d + 15) / 16;
     const bool paged = b < (n >> 5);
     uint8_t* page = nullptr;
     if (paged && !(page = b8_page(c, c.table[s * c.max_blocks + b]))) return;
-    const int64_t row = (s * p.n_tok + j) * c.n_kv * c.d;
+    const int64_t row0 = (s * p.n_tok + pos - (n - p.n_tok)) * c.n_kv * c.d;
+    void* out = side ? p.v : p.k;
     for (int i = lane; i < c.n_kv * chunks; i += 32) {
         const int h = i / chunks, ch = i - h * chunks;
-        float f[8];
+        const bool both = 16 * ch + 8 < c.d;             // d may end in the middle of the 16 channels
         if (paged) {
             const float sc = *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side);
-            const uint2 w = *reinterpret_cast<const uint2*>(b8_codes(c, page, h, side) + t * D +
-                                                            (((ch >> 1) ^ b8_swz(t, D / 16)) << 4) + (ch & 1) * 8);
+            const uint8_t* codes = b8_codes(c, page, h, side);
+            uint4 w[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = sc * (float)((int)(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 0xffu) - 128);
+            for (int t = 0; t < 4; ++t)
+                w[t] = tq_ldg_stream(codes + (t0 + t) * D + ((ch ^ b8_swz(t0 + t, D / 16)) << 4));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (pos + t < from || pos + t >= n) continue;
+                const uint32_t u[4] = {w[t].x, w[t].y, w[t].z, w[t].w};
+                float f[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    f[k] = sc * (__uint_as_float(__byte_perm(u[k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f);
+                const int64_t at = row0 + (int64_t)t * c.n_kv * c.d + (int64_t)h * c.d + 16 * ch;
+                if (F32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+                    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    if (both) {
+                        o[2] = make_float4(f[8], f[9], f[10], f[11]);
+                        o[3] = make_float4(f[12], f[13], f[14], f[15]);
+                    }
+                } else {
+                    __nv_bfloat162 r[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) r[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+                    o[0] = *reinterpret_cast<uint4*>(r);
+                    if (both) o[1] = *reinterpret_cast<uint4*>(r + 4);
+                }
+            }
         } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(b8_open(c, s, h, side) + t * c.d + ch * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(k & 1 ? u[k >> 1] & 0xffff0000u : u[k >> 1] << 16);
-        }
-        const int64_t at = row + (int64_t)h * c.d + ch * 8;
-        if (F32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(side ? p.v : p.k) + at);
-            o[0] = make_float4(f[0], f[1], f[2], f[3]);
-            o[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            __nv_bfloat162 r[4];
+            for (int t = 0; t < 4; ++t) {
+                if (pos + t < from || pos + t >= n) continue;
+                const uint4* src = reinterpret_cast<const uint4*>(b8_open(c, s, h, side) + (t0 + t) * c.d + 16 * ch);
+                const int64_t at = row0 + (int64_t)t * c.n_kv * c.d + (int64_t)h * c.d + 16 * ch;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(side ? p.v : p.k) + at) = *reinterpret_cast<uint4*>(r);
+                for (int k = 0; k < 2; ++k) {
+                    if (k && !both) break;
+                    const uint4 x = src[k];
+                    if (F32) {
+                        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 8 * k);
+                        o[0] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                                           __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+                        o[1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
+                                           __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u));
+                    } else {
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + 8 * k) = x;
+                    }
+                }
+            }
         }
     }
 }
@@ -227,8 +261,9 @@ cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st) {
 }
 
 cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st) {
-    const int64_t grid = (p.c.n_seq * p.n_tok * 2 + kReadWarps - 1) / kReadWarps;
+    const int64_t groups = (p.n_tok + 3) / 4 + 1;   // the first and the last may be cut
+    const int64_t grid = (p.c.n_seq * groups * 2 + kReadWarps - 1) / kReadWarps;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    B8_DISPATCH(k_b8_read, (unsigned)grid, kReadWarps * 32, 0, st>>>(p));
+    B8_DISPATCH(k_b8_read, (unsigned)grid, kReadWarps * 32, 0, st>>>(p, groups));
     return cudaGetLastError();
 }

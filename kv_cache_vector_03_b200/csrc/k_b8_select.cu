@@ -17,7 +17,7 @@
 namespace {
 
 constexpr int kScoreWarps = 8;
-constexpr int kPickThreads = 512;
+constexpr int kPickThreads = 1024;
 constexpr int kMoveWarps = 4;
 constexpr float kRound = 12583040.f;     // 1.5 * 2^23 + 128: a sum's low byte is code + 128
 
@@ -116,103 +116,121 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
     }
 }
 
-// ascending indices of the chosen of n: all of them if n <= k, else the first nf, the last nl and
-// the k - nf - nl largest keys between, ties to the lowest; the rest of out[0 .. k) is -1
+// Ascending indices of the chosen of n: all of them if n <= k, else the first nf, the last nl and the
+// k - nf - nl largest keys between, ties to the lowest; the rest of out[0 .. k) is -1. A thread holds 16 keys in
+// registers; up to 16384 keys are read once, more once for each digit.
+constexpr int kPickKeys = 16, kPickChunk = kPickKeys * kPickThreads;
 template <typename Key>
-TQ_DEVICE void pick(int64_t n, int64_t k, int64_t nf, int64_t nl, Key key, int32_t* out) {
-    __shared__ uint32_t s_hist[2048], s_cnt[2][kPickThreads / 32], s_digit, s_left;
+TQ_DEVICE void pick(int n, int64_t k64, int nf, int nl, Key key, int32_t* out) {
+    __shared__ uint32_t s_hist[2048], s_cnt[kPickKeys][32], s_tot[kPickKeys], s_warp[32], s_digit, s_left;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    if (n <= k) {
-        for (int64_t j = tid; j < k; j += kPickThreads) out[j] = j < n ? (int32_t)j : -1;
+    if (n <= k64) {
+        for (int64_t j = tid; j < k64; j += kPickThreads) out[j] = j < n ? (int32_t)j : -1;
         return;
     }
-    const int64_t m0 = nf, m1 = n - nl;
+    const int k = (int)k64, m0 = nf, m1 = n - nl;
     uint32_t left = (uint32_t)(k - nf - nl);      // how many the middle gives
-    uint32_t prefix = 0, mask = 0;
+    uint32_t prefix = 0, mask = 0, u[kPickKeys];
     const bool any = left > 0;
-    if (any) {
-        for (int pass = 0; pass < 3; ++pass) {
-            const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            for (int b = tid; b < 2048; b += kPickThreads) s_hist[b] = 0;
-            __syncthreads();
-            for (int64_t t = m0 + tid; t < m1; t += kPickThreads) {
-                const uint32_t u = key(t);
-                if ((u & mask) == prefix) atomicAdd(&s_hist[(u >> sh) & ((1u << bits) - 1)], 1u);
-            }
-            __syncthreads();
-            // the largest digit with at least `left` keys at or above it: one warp, from the top
-            if (w == 0) {
-                uint32_t above = 0;
-                for (int b = 2048 - 32; b >= 0; b -= 32) {
-                    const uint32_t v = s_hist[b + 31 - lane];      // lane 0 holds the highest bin
-                    uint32_t sum = v;
+    auto load = [&](int c0) {
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-                        if (lane >= o) sum += x;
-                    }
-                    const uint32_t hit = __ballot_sync(0xffffffffu, above + sum >= left);
-                    if (hit) {
-                        const int f = __ffs(hit) - 1;
-                        const uint32_t before = above + __shfl_sync(0xffffffffu, sum - v, f);
-                        if (lane == 0) {
-                            s_digit = b + 31 - f;
-                            s_left = left - before;
-                        }
-                        break;
-                    }
-                    above += __shfl_sync(0xffffffffu, sum, 31);
+        for (int i = 0; i < kPickKeys; ++i) {
+            const int t = c0 + i * kPickThreads + tid;
+            u[i] = t >= m0 && t < m1 ? key(t) : 0u;
+        }
+    };
+    if (any) {
+        load(0);
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digit = pass == 2 ? 1023u : 2047u;
+            s_hist[tid] = s_hist[tid + 1024] = 0;
+            __syncthreads();
+#pragma unroll 1
+            for (int c0 = 0; c0 < n; c0 += kPickChunk) {
+                if (n > kPickChunk) load(c0);
+#pragma unroll
+                for (int i = 0; i < kPickKeys; ++i) {
+                    const int t = c0 + i * kPickThreads + tid;
+                    if (t >= m0 && t < m1 && (u[i] & mask) == prefix) atomicAdd(&s_hist[(u[i] >> sh) & digit], 1u);
                 }
             }
             __syncthreads();
-            prefix |= s_digit << sh;
-            mask |= ((1u << bits) - 1) << sh;
-            left = s_left;
+            // the largest digit with at least `left` keys at or above it: thread t sums the bins 2047 - 2 t, 2046 - 2 t
+            const uint32_t hi = s_hist[2047 - 2 * tid], lo = s_hist[2046 - 2 * tid];
+            uint32_t incl = hi + lo;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            if (lane == 31) s_warp[w] = incl;
             __syncthreads();
+            const uint32_t above = incl - hi - lo + __reduce_add_sync(0xffffffffu, lane < w ? s_warp[lane] : 0u);
+            if (above < left && above + hi + lo >= left) {
+                const bool first = above + hi >= left;
+                s_digit = 2047 - 2 * tid - (first ? 0 : 1);
+                s_left = left - above - (first ? 0 : hi);
+            }
+            __syncthreads();
+            prefix |= s_digit << sh;
+            mask |= digit << sh;
+            left = s_left;
         }
     }
-    // `left` keys equal to prefix are still wanted, the lowest indices first
-    int64_t done = 0;
-    uint32_t ties = 0;
-    for (int64_t t0 = 0; t0 < n; t0 += kPickThreads) {
-        const int64_t t = t0 + tid;
-        bool take = t < n && (t < nf || t >= m1), tie = false;
-        if (any && t >= m0 && t < m1) {
-            const uint32_t u = key(t);
-            take = u > prefix;
-            tie = u == prefix;
+    // What lies above prefix is taken, and the first `left` of what equals it: an index's place is the number
+    // taken for sure before it plus the number of ties before it, up to `left`.
+    const uint32_t below = (1u << lane) - 1;
+    uint32_t sure0 = 0, ties0 = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += kPickChunk) {
+        if (any && n > kPickChunk) load(c0);
+        uint32_t is_sure = 0, is_tie = 0;            // a bit per key
+#pragma unroll
+        for (int i = 0; i < kPickKeys; ++i) {
+            const int t = c0 + i * kPickThreads + tid;
+            const bool mid = any && t >= m0 && t < m1;
+            const bool sure = t < n && (t < m0 || t >= m1 || (mid && u[i] > prefix)), tie = mid && u[i] == prefix;
+            const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
+            if (lane == 0) s_cnt[i][w] = __popc(bs) | __popc(bt) << 16;
+            is_sure |= (uint32_t)sure << i;
+            is_tie |= (uint32_t)tie << i;
         }
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t bt = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) s_cnt[0][w] = __popc(bt);
         __syncthreads();
-        uint32_t rank = ties, all = ties;
-        for (int v = 0; v < kPickThreads / 32; ++v) {
-            if (v < w) rank += s_cnt[0][v];
-            all += s_cnt[0][v];
+        if (w < kPickKeys) {
+            const uint32_t v = s_cnt[w][lane];
+            uint32_t incl = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            s_cnt[w][lane] = incl - v;
+            if (lane == 31) s_tot[w] = incl;
         }
-        rank += __popc(bt & below);
-        take = take || (tie && rank < left);
-        ties = all;
-        const uint32_t bk = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) s_cnt[1][w] = __popc(bk);
         __syncthreads();
-        int64_t at = done;
-        for (int v = 0; v < kPickThreads / 32; ++v) {
-            if (v < w) at += s_cnt[1][v];
-            done += s_cnt[1][v];
+#pragma unroll
+        for (int i = 0; i < kPickKeys; ++i) {
+            const bool sure = is_sure >> i & 1u, tie = is_tie >> i & 1u;
+            const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
+            const uint32_t c = s_cnt[i][w], ties = ties0 + (c >> 16) + __popc(bt & below);
+            if (sure || (tie && ties < left))
+                out[sure0 + (c & 0xffffu) + __popc(bs & below) + min(ties, left)] = c0 + i * kPickThreads + tid;
+            sure0 += s_tot[i] & 0xffffu;
+            ties0 += s_tot[i] >> 16;
         }
-        if (take) out[at + __popc(bk & below)] = (int32_t)t;
+        __syncthreads();
     }
 }
 
 struct ScoreKey {
     const uint32_t* key;
-    TQ_DEVICE uint32_t operator()(int64_t t) const { return key[t]; }
+    TQ_DEVICE uint32_t operator()(int t) const { return key[t]; }
 };
 struct WeightKey {
     const float* acc;
-    TQ_DEVICE uint32_t operator()(int64_t t) const { return __float_as_uint(fmaxf(acc[t], 0.f) + 0.f); }
+    TQ_DEVICE uint32_t operator()(int t) const { return __float_as_uint(fmaxf(acc[t], 0.f) + 0.f); }
 };
 
 __global__ void __launch_bounds__(kPickThreads) k_b8_pick_blocks(const __grid_constant__ B8SelectParams p) {
@@ -224,13 +242,30 @@ __global__ void __launch_bounds__(kPickThreads) k_b8_pick_blocks(const __grid_co
 __global__ void __launch_bounds__(kPickThreads) k_b8_pick_tokens(const __grid_constant__ B8EvictParams p) {
     const int64_t row = blockIdx.x, s = row / p.c.n_kv;
     const int n = b8_len(p.c, s) & ~31;
-    pick(n, 32 * p.keep_blocks, p.n_first, p.n_last, WeightKey{p.acc + row * p.c.max_blocks * 32},
+    // (n_first and n_last are at most the tokens kept, and matter where there are more than those)
+    pick(n, 32 * p.keep_blocks, (int)p.n_first, (int)p.n_last, WeightKey{p.acc + row * p.c.max_blocks * 32},
          p.kept + row * 32 * p.keep_blocks);
 }
+
+// max(|c|) over the bytes c + 128 of a word, in the larger of two 16-bit halves: lo and hi run over words
+struct ByteRange {
+    uint32_t lo, hi;                                 // 16-bit minima and maxima of the even and odd bytes
+    TQ_DEVICE void take(uint32_t w) {
+        const uint32_t e = w & 0x00ff00ffu, o = __byte_perm(w, 0, 0x4341);
+        lo = __vminu2(lo, __vminu2(e, o));
+        hi = __vmaxu2(hi, __vmaxu2(e, o));
+    }
+    TQ_DEVICE int top() const {                      // the largest |c|
+        const int l = (int)min(lo & 0xffffu, lo >> 16), h = (int)max(hi & 0xffffu, hi >> 16);
+        return max(h - 128, 128 - l);
+    }
+};
 
 // One warp per (sequence, new block, keys or values, head): gathers 32 kept tokens, finds the new
 // scale, requantizes by one multiply-add per code and writes the block, its scale and summary.
 // The warps of new block keep_blocks move what belongs to the open block: its acc, the length.
+// A lane holds 16 channels of D / 16 tokens; codes stay packed but for the multiply-add, maxima and the
+// summary's ranges are taken on 16-bit pairs.
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_constant__ B8EvictParams p) {
     constexpr int CH = D / 16, TPI = 32 / CH, IT = CH;   // 16-byte chunks of a row; tokens per step; steps
@@ -253,42 +288,43 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
     }
     if (j >= left) return;
     const int tok = p.kept[((s * c.n_kv + h) * p.keep_blocks + j) * 32 + lane];
-    if (side == 0) p.acc_out[arow + 32 * j + lane] = p.acc[arow + tok];
     uint8_t* page = b8_page(c, c.table[s * c.max_blocks + (tok >> 5)]);
     uint8_t* dst = b8_page(c, p.dst_table[s * c.max_blocks + j]);
     const float sc = page ? *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side) : 0.f;
     const uint8_t* row = page ? b8_codes(c, page, h, side) + (tok & 31) * D : nullptr;
     const int ch = lane % CH, t0 = lane / CH;
     uint4 x[IT];
-    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int t = t0 + i * TPI;
         const uint8_t* rp = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)row, t));
         const int tk = __shfl_sync(0xffffffffu, tok, t) & 31;
-        x[i] = rp ? *reinterpret_cast<const uint4*>(rp + ((ch ^ b8_swz(tk, CH)) << 4))
+        x[i] = rp ? tq_ldg_stream(rp + ((ch ^ b8_swz(tk, CH)) << 4))
                   : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
     }
+    if (side == 0) p.acc_out[arow + 32 * j + lane] = p.acc[arow + tok];
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float m = 0.f;
+        ByteRange br = {0x00ff00ffu, 0u};
+        br.take(x[i].x);
+        br.take(x[i].y);
+        br.take(x[i].z);
+        br.take(x[i].w);
+        int m = br.top();
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            m = fmaxf(m, fabsf(__uint_as_float(__byte_perm(u[k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f));
-#pragma unroll
-        for (int o = 1; o < CH; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        top = fmaxf(top, __fmul_rn(__fmul_rn(m, kB8Inv127), __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
+        for (int o = 1; o < CH; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        top = fmaxf(top, __fmul_rn(__fmul_rn((float)m, kB8Inv127), __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
     }
     top = tq_warp_max(top);
     if (!dst) return;
     const float ratio = top > 0.f ? sc / top : 0.f;
     uint8_t* drow = b8_codes(c, dst, h, side);
-    float lo[16], hi[16];
+    uint32_t lo[8], hi[8];                               // 16-bit ranges of this lane's 16 channels
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        lo[k] = INFINITY;
-        hi[k] = -INFINITY;
+    for (int k = 0; k < 8; ++k) {
+        lo[k] = 0x00ff00ffu;
+        hi[k] = 0u;
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -300,14 +336,17 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
         for (int q = 0; q < 4; ++q) {
             float f[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float cd = __uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f;
-                f[k] = fmaf(cd, rt, kRound);
-                lo[4 * q + k] = fminf(lo[4 * q + k], f[k]);
-                hi[4 * q + k] = fmaxf(hi[4 * q + k], f[k]);
-            }
+            for (int k = 0; k < 4; ++k)
+                f[k] = fmaf(__uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f, rt, kRound);
             o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
                                __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
+            if (side == 0) {
+                const uint32_t e = o[q] & 0x00ff00ffu, d = __byte_perm(o[q], 0, 0x4341);
+                lo[2 * q] = __vminu2(lo[2 * q], e);
+                hi[2 * q] = __vmaxu2(hi[2 * q], e);
+                lo[2 * q + 1] = __vminu2(lo[2 * q + 1], d);
+                hi[2 * q + 1] = __vmaxu2(hi[2 * q + 1], d);
+            }
         }
         *reinterpret_cast<uint4*>(drow + t * D + ((ch ^ b8_swz(t, CH)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -315,22 +354,18 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
     if (lane == 0) *reinterpret_cast<float*>(e + 4 * side) = top;
     if (side) return;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int o = CH; o < 32; o <<= 1) {
-            lo[k] = fminf(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
-            hi[k] = fmaxf(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+            lo[k] = __vminu2(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+            hi[k] = __vmaxu2(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
         }
     if (lane < CH) {
         uint32_t l[4], g[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            l[q] = g[q] = 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                l[q] |= ((__float_as_uint(lo[4 * q + k]) ^ 0x80u) & 0xffu) << (8 * k);
-                g[q] |= ((__float_as_uint(hi[4 * q + k]) ^ 0x80u) & 0xffu) << (8 * k);
-            }
+        for (int q = 0; q < 4; ++q) {                    // even bytes from one pair, odd bytes from the other
+            l[q] = (lo[2 * q] | lo[2 * q + 1] << 8) ^ 0x80808080u;
+            g[q] = (hi[2 * q] | hi[2 * q + 1] << 8) ^ 0x80808080u;
         }
         *reinterpret_cast<uint4*>(e + 32 + 16 * ch) = make_uint4(l[0], l[1], l[2], l[3]);
         *reinterpret_cast<uint4*>(e + 32 + D + 16 * ch) = make_uint4(g[0], g[1], g[2], g[3]);
