@@ -4,7 +4,7 @@
 #include "tq_device.cuh"
 
 constexpr int kB8Block = 32;
-constexpr int kB8Counters = 192;   // arrival counts (a byte each) behind the status word, in its 256 bytes
+constexpr int kB8Counters = 192;   // bytes of arrival counts (4 bits a CTA) behind the status word, in its 256 bytes
 constexpr float kB8Inv127 = 1.f / 127.f;               // rounded to fp32; 127 times it rounds to 1
 constexpr float kB8MinMax = 7.8886090522101181e-31f;   // 2^-100: a block whose largest |x| is below it is stored as zeros
 
@@ -82,7 +82,7 @@ struct B8AttnParams {
     int64_t logit_row;
     float* part;             // [2 grid][row_tile][D] partial value sums, [2 grid][row_tile][2] their maximum and sum
     float* part_ml;
-    uint32_t* count;         // kB8Counters bytes, zero between calls: parts of a segment that have arrived
+    uint32_t* count;         // kB8Counters bytes, zero between calls: how many parts of a segment have arrived
     int grid, row_tile, row_tiles;
 };
 struct B8SelectParams {

@@ -17,6 +17,7 @@
 // are split into two fp16 pieces too: one piece alone is off by 2^-12, which an fp32 output shows.
 // Scales multiply after the products: the key scale on the logits (as a product kept in two
 // floats, so that large logits lose nothing), the value scale on each block's partial sum.
+#include <algorithm>
 #include <cfloat>
 
 #include "k_b8.cuh"
@@ -26,16 +27,18 @@ namespace {
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kBias = 7.f;         // weights are kept as 2^(7 + logit - m): their small pieces stay normal in fp16
 constexpr float kSlack = 8.f;        // m follows the maximum once it is passed by 2^8: 2^(7 + 8) < 65504
-constexpr int kMinUnits = 16;        // units a CTA takes at least, where segments are shared
+constexpr int kMinUnits = 8;        // units a CTA takes at least, where segments are shared
 constexpr int kStraddle = 24;
 constexpr int kWholeUnits = 32;      // segments up to here are not shared
 constexpr int kAccTok = 256;
 
-// Warps, the CTA's ring of pages, and in how many rounds the warps' sums meet in shared memory
+// Two CTAs share an SM, so that one computes while the other starts or joins a segment. Warps and ring stages of
+// one of them, and in how many rounds its warps' sums meet in shared memory.
+constexpr int kCtasPerSm = 2;
 template <int D, int NT>
 struct Shape {
-    static constexpr int warps = D == 256 ? 8 : NT == 2 && D == 128 ? 12 : 16;
-    static constexpr int stages = D == 64 ? 40 : D == 128 ? 20 : 10;
+    static constexpr int warps = D == 256 ? 4 : NT == 2 && D == 128 ? 6 : 8;
+    static constexpr int stages = D == 64 ? 20 : D == 128 ? 10 : 5;
     static constexpr int stage_bytes = 64 * D + 128;   // keys, values, scales
     static constexpr int rounds = NT * D == 64 ? 1 : NT * D == 128 ? 2 : D == 256 ? 2 : 4;
     static constexpr size_t smem = (size_t)stages * stage_bytes + (size_t)warps * 8 * NT * (D / rounds + 4) * 4;
@@ -110,7 +113,8 @@ struct Plan {
     }
 };
 // Sums the units of all virtual sequences and finds this CTA's share of them, one of three ways:
-//   segments of up to kWholeUnits units: shares begin and end between segments, nothing is joined;
+//   short segments (up to kWholeUnits units), or so many that whole ones come out even: shares begin and end
+//     between segments, nothing is joined;
 //   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length. A CTA
 //     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
 //     everyone would wait for it;
@@ -155,8 +159,9 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
     __syncthreads();
     longest = (int)__reduce_max_sync(0xffffffffu, lane < NW ? s_max[lane] : 0);
     const bool one = n_virt <= THREADS;              // units and incl are this thread's virtual sequence's
-    const bool whole = longest <= kWholeUnits;
     const int n_segs = n_virt * segs;
+    const bool whole = longest <= kWholeUnits ||
+                       (n_segs > p.grid && (n_segs + p.grid - 1) / p.grid * longest <= total / p.grid + kStraddle);
     if (!whole && n_segs <= p.grid) {                // (then n_virt <= THREADS)
         // 1 + floor(units (grid - segments) / total) parts each are never more than the grid together
         const int spare = min(p.grid, total / kMinUnits) - n_segs;
@@ -231,7 +236,7 @@ struct __align__(8) Record {
 };
 
 template <int D, int NT, bool WT>
-__global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const __grid_constant__ B8AttnParams p) {
+__global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_attn(const __grid_constant__ B8AttnParams p) {
     using Sh = Shape<D, NT>;
     constexpr int NW = Sh::warps, ST = Sh::stages, SB = Sh::stage_bytes, RD = Sh::rounds;
     constexpr int MT = D / 16;           // m-tiles of O^T
@@ -800,8 +805,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const _
         const bool whole = part == units;
         const size_t slot = 2 * (size_t)blockIdx.x + (off == 0 ? 1 : 0);
         constexpr int LC = 2 * MT / RD, RS = 8 * LC + 4;  // channels of a lane per round; a row's pitch
-        constexpr int G = NW == 16 ? 4 : NW == 12 ? 2 : 1, items = 8 * NT * 2 * LC;
-        static_assert(items * G <= NW * 32, "one pass");
+        constexpr int G = NW == 8 ? 2 : 1, items = 8 * NT * 2 * LC;   // G threads share an item
 #pragma unroll
         for (int rd = 0; rd < RD; ++rd) {
             if (rd) __syncthreads();
@@ -819,8 +823,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const _
                     }
                 }
             __syncthreads();
-            const int t = threadIdx.x / G, xg = threadIdx.x % G, r = t / (2 * LC), cg = t % (2 * LC) / (LC / 4), c4 = t % (LC / 4) * 4;
-            if (t < items && row0 + r < rows) {           // (the G threads of an item are neighbours in a warp)
+            const int xg = threadIdx.x % G;
+            for (int t = threadIdx.x / G; t < items; t += NW * 32 / G) {
+                const int r = t / (2 * LC), cg = t % (2 * LC) / (LC / 4), c4 = t % (LC / 4) * 4;
+                if (row0 + r >= rows) continue;           // (the G threads of an item are neighbours in a warp)
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < NW / G; ++y) {
@@ -860,34 +866,35 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const _
         }
         __syncthreads();                                  // s_o and the row sums are free again
         if (!whole) {
-            // The CTA that brings a segment's last part joins all of them, in their order. The count of a
-            // segment that begins in CTA c0 and goes on is byte c0 of the workspace's counters, back at 0 after.
+            // The CTA that brings a segment's last part joins all of them, in their order. The arrival count of a
+            // segment is back at 0 after.
             const int first = pl.u0 + u - off;
             const int c0 = pl.c0 >= 0 ? pl.c0 : pl.owner(first), c1 = pl.c0 >= 0 ? pl.c1 : pl.owner(first + units - 1);
             if (threadIdx.x == 0) {
-                const uint32_t sh = 8 * (c0 & 3);
-                const uint32_t got = (atomic_add_acq_rel(p.count + (c0 >> 2), 1u << sh) >> sh & 255u) + 1;
-                s_last = (int)got == c1 - c0 + 1;
-                if (s_last) atomicSub(p.count + (c0 >> 2), got << sh);
+                // The 4-bit fields of CTAs c0 .. c1 - 1 are this segment's alone: one counts up to 15 parts, and
+                // in 15 fields or more there is a whole 16-bit one.
+                const int parts = c1 - c0 + 1, bit = parts < 16 ? 4 * c0 : (4 * c0 + 15) & ~15, sh = bit & 31;
+                const uint32_t field = parts < 16 ? 15u : 65535u;
+                const uint32_t got = (atomic_add_acq_rel(p.count + (bit >> 5), 1u << sh) >> sh & field) + 1;
+                s_last = (int)got == parts;
+                if (s_last) atomicSub(p.count + (bit >> 5), got << sh);
             }
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                float2* fac = reinterpret_cast<float2*>(s_o);   // [part][row]: maximum and sum, then the factor
+                auto ml_at = [&](int x, int r) {                // maximum and sum of part x; then the factor instead
+                    return reinterpret_cast<float2*>(p.part_ml + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * 2);
+                };
                 for (int r = w; r < 8 * NT && row0 + r < rows; r += NW) {
                     float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-                    for (int x = c0 + lane; x <= c1; x += 32) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * 2));
-                        fac[(x - c0) * 8 * NT + r] = ml;
-                        top = fmaxf(top, ml.x);
-                    }
+                    for (int x = c0 + lane; x <= c1; x += 32) top = fmaxf(top, __ldcg(ml_at(x, r)).x);
                     top = tq_warp_max(top);
 #pragma unroll 1
                     for (int x = c0 + lane; x <= c1; x += 32) {
-                        const float2 ml = fac[(x - c0) * 8 * NT + r];
+                        const float2 ml = __ldcg(ml_at(x, r));
                         const float y = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : tq_exp2(ml.x - top);
-                        fac[(x - c0) * 8 * NT + r].x = y;
+                        __stcg(&ml_at(x, r)->x, y);
                         sum = y == 0.f ? sum : fmaf(ml.y, y, sum);
                     }
                     sum = tq_warp_sum(sum);
@@ -904,9 +911,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, 1) k_b8_attn(const _
                     if (row0 + r < rows) {
 #pragma unroll 4
                         for (int x = c0 + (t & 3); x <= c1; x += 4) {
-                            const float y = fac[(x - c0) * 8 * NT + r].x;
+                            const float y = __ldcg(&ml_at(x, r)->x);
                             const float4 z = __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * D + e));
-                            a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
+                            if (y != 0.f) {
+                                a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
+                            }
                         }
                     }
 #pragma unroll
@@ -986,7 +995,7 @@ cudaError_t launch(const B8AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 int b8_attn_row_tile(int D, int rows) { return rows <= 8 || D == 256 ? 8 : 16; }
-int b8_attn_grid() { return tq_device_sms() < kB8Counters ? tq_device_sms() : kB8Counters; }
+int b8_attn_grid() { return std::min(kCtasPerSm * tq_device_sms(), 2 * kB8Counters); }
 
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     const int64_t virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
