@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     }
     tq_fence_mbar_init();
     tq_pdl_launch_dependents();
+    tq_pdl_wait();                                   // nothing is read before the kernel in front is done
 
     const int segs = c.n_kv * p.row_tiles;
     const int n_virt = (int)(p.sel ? c.n_seq * p.n_q : c.n_seq);
@@ -905,17 +906,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 }
                 __syncthreads();
 #pragma unroll 1
-                for (int t = threadIdx.x; t < 8 * NT * D; t += NW * 32) {      // 4 threads per (row, 4 channels)
+                for (int t = threadIdx.x; t < min(8 * NT, rows - row0) * D; t += NW * 32) {   // 4 threads per (row, 4 channels)
                     const int r = t / D, e = t % D / 4 * 4;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (row0 + r < rows) {
-#pragma unroll 4
-                        for (int x = c0 + (t & 3); x <= c1; x += 4) {
-                            const float y = __ldcg(&ml_at(x, r)->x);
-                            const float4 z = __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * D + e));
-                            if (y != 0.f) {
-                                a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
-                            }
+#pragma unroll 8
+                    for (int x = c0 + (t & 3); x <= c1; x += 4) {
+                        const float y = __ldcg(&ml_at(x, r)->x);
+                        const float4 z = __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * D + e));
+                        if (y != 0.f) {
+                            a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
                         }
                     }
 #pragma unroll
@@ -923,7 +922,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                         a.x += __shfl_xor_sync(0xffffffffu, a.x, d); a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
                         a.z += __shfl_xor_sync(0xffffffffu, a.z, d); a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
                     }
-                    if ((t & 3) == 0 && row0 + r < rows && e < c.d) {
+                    if ((t & 3) == 0 && e < c.d) {
                         const float inv = s_sum[r] == 0.f ? 0.f : 1.f / s_sum[r];
                         *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r) * c.d + e) =
                             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
@@ -948,6 +947,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 // its entries holds a block.
 __global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int64_t tiles) {
     const B8Cache& c = p.c;
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
     const int64_t sh = blockIdx.x / tiles, s = sh / c.n_kv;
     const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g;
     const int64_t t0 = (blockIdx.x - sh * tiles) * kAccTok, t = t0 + threadIdx.x;
@@ -984,8 +985,7 @@ cudaError_t launch_one(const B8AttnParams& p, cudaStream_t st) {
     static TqLaunchCache cache;
     const cudaError_t e = tq_kernel_setup(k_b8_attn<D, NT, WT>, Sh::warps * 32, Sh::smem, cache, nullptr, nullptr);
     if (e != cudaSuccess) return e;
-    k_b8_attn<D, NT, WT><<<(unsigned)p.grid, Sh::warps * 32, Sh::smem, st>>>(p);
-    return cudaGetLastError();
+    return tq_launch_pdl(k_b8_attn<D, NT, WT>, dim3((unsigned)p.grid), dim3(Sh::warps * 32), Sh::smem, st, p);
 }
 template <int D, int NT>
 cudaError_t launch(const B8AttnParams& p, cudaStream_t st) {
@@ -1011,6 +1011,5 @@ cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     else if (p.c.D == 128) e = wide ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
     else e = launch<256, 1>(p, st);
     if (e != cudaSuccess || !p.acc_out) return e;
-    k_b8_acc<<<(unsigned)(tiles * p.c.n_seq * p.c.n_kv), kAccTok, 0, st>>>(p, tiles);
-    return cudaGetLastError();
+    return tq_launch_pdl(k_b8_acc, dim3((unsigned)(tiles * p.c.n_seq * p.c.n_kv)), dim3(kAccTok), 0, st, p, tiles);
 }

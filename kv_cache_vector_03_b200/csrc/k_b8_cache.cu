@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
     constexpr int CH = D / 8;        // 8-channel chunks of a row; also token steps of a lane
     constexpr int TPI = 32 / CH;     // tokens of one step
     const B8Cache& c = p.c;
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
     const int lane = threadIdx.x & 31;
     int64_t id = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int h = (int)(id % c.n_kv);
@@ -162,6 +164,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
 template <int D, bool F32>
 __global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p, int64_t groups) {
     const B8Cache& c = p.c;
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
     const int lane = threadIdx.x & 31;
     int64_t id = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
     const int side = (int)(id & 1);
@@ -241,29 +245,25 @@ __global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_consta
 
 }  // namespace
 
-#define B8_DISPATCH(KERN, ...)                                                                     \
-    do {                                                                                           \
-        if (p.c.D == 64) {                                                                         \
-            if (p.dtype) KERN<64, false><<<__VA_ARGS__; else KERN<64, true><<<__VA_ARGS__;         \
-        } else if (p.c.D == 128) {                                                                 \
-            if (p.dtype) KERN<128, false><<<__VA_ARGS__; else KERN<128, true><<<__VA_ARGS__;       \
-        } else {                                                                                   \
-            if (p.dtype) KERN<256, false><<<__VA_ARGS__; else KERN<256, true><<<__VA_ARGS__;       \
-        }                                                                                          \
-    } while (0)
+// kern<D, input or output in fp32>(p, more...) as a programmatic dependent of the kernel in front
+#define B8_LAUNCH(KERN, GRID, WARPS, ...)                                                                              \
+    (p.c.D == 64    ? tq_launch_pdl(p.dtype ? KERN<64, false> : KERN<64, true>, dim3(GRID), dim3(WARPS * 32), 0, st,   \
+                                    __VA_ARGS__)                                                                       \
+     : p.c.D == 128 ? tq_launch_pdl(p.dtype ? KERN<128, false> : KERN<128, true>, dim3(GRID), dim3(WARPS * 32), 0, st, \
+                                    __VA_ARGS__)                                                                       \
+                    : tq_launch_pdl(p.dtype ? KERN<256, false> : KERN<256, true>, dim3(GRID), dim3(WARPS * 32), 0, st, \
+                                    __VA_ARGS__))
 
 cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st) {
     const int64_t nbt = (p.n_new + 62) / 32;   // a call touches at most this many blocks of a sequence
     const int64_t grid = (p.c.n_seq * nbt * 2 * p.c.n_kv + kAppendWarps - 1) / kAppendWarps;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    B8_DISPATCH(k_b8_append, (unsigned)grid, kAppendWarps * 32, 0, st>>>(p, (int)nbt));
-    return cudaGetLastError();
+    return B8_LAUNCH(k_b8_append, (unsigned)grid, kAppendWarps, p, (int)nbt);
 }
 
 cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st) {
     const int64_t groups = (p.n_tok + 3) / 4 + 1;   // the first and the last may be cut
     const int64_t grid = (p.c.n_seq * groups * 2 + kReadWarps - 1) / kReadWarps;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    B8_DISPATCH(k_b8_read, (unsigned)grid, kReadWarps * 32, 0, st>>>(p, groups));
-    return cudaGetLastError();
+    return B8_LAUNCH(k_b8_read, (unsigned)grid, kReadWarps, p, groups);
 }

@@ -17,7 +17,6 @@
 namespace {
 
 constexpr int kScoreWarps = 8;
-constexpr int kPickThreads = 1024;
 constexpr int kMoveWarps = 4;
 constexpr float kRound = 12583040.f;     // 1.5 * 2^23 + 128: a sum's low byte is code + 128
 
@@ -36,6 +35,8 @@ template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int tiles) {
     constexpr int CH = D / 32;       // 16-byte chunks a lane takes of a summary's 2 D bytes
     const B8Cache& c = p.c;
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     int64_t rowid = blockIdx.x / tiles;
     const int tile = (int)(blockIdx.x - rowid * tiles);
@@ -117,25 +118,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
 }
 
 // Ascending indices of the chosen of n: all of them if n <= k, else the first nf, the last nl and the
-// k - nf - nl largest keys between, ties to the lowest; the rest of out[0 .. k) is -1. A thread holds 16 keys in
-// registers; up to 16384 keys are read once, more once for each digit.
-constexpr int kPickKeys = 16, kPickChunk = kPickKeys * kPickThreads;
-template <typename Key>
+// k - nf - nl largest keys between, ties to the lowest; the rest of out[0 .. k) is -1. A thread holds KEYS keys in
+// registers; up to KEYS * THREADS keys are read once, more once for each digit.
+template <int THREADS, int KEYS, typename Key>
 TQ_DEVICE void pick(int n, int64_t k64, int nf, int nl, Key key, int32_t* out) {
-    __shared__ uint32_t s_hist[2048], s_cnt[kPickKeys][32], s_tot[kPickKeys], s_warp[32], s_digit, s_left;
+    constexpr int NW = THREADS / 32, BINS = 2048 / THREADS, CHUNK = KEYS * THREADS;
+    __shared__ uint32_t s_hist[2048], s_cnt[KEYS][NW], s_tot[KEYS], s_warp[NW], s_digit, s_left, s_here;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (n <= k64) {
-        for (int64_t j = tid; j < k64; j += kPickThreads) out[j] = j < n ? (int32_t)j : -1;
+        for (int64_t j = tid; j < k64; j += THREADS) out[j] = j < n ? (int32_t)j : -1;
         return;
     }
     const int k = (int)k64, m0 = nf, m1 = n - nl;
     uint32_t left = (uint32_t)(k - nf - nl);      // how many the middle gives
-    uint32_t prefix = 0, mask = 0, u[kPickKeys];
+    uint32_t prefix = 0, mask = 0, u[KEYS];
     const bool any = left > 0;
     auto load = [&](int c0) {
 #pragma unroll
-        for (int i = 0; i < kPickKeys; ++i) {
-            const int t = c0 + i * kPickThreads + tid;
+        for (int i = 0; i < KEYS; ++i) {
+            const int t = c0 + i * THREADS + tid;
             u[i] = t >= m0 && t < m1 ? key(t) : 0u;
         }
     };
@@ -145,21 +146,27 @@ TQ_DEVICE void pick(int n, int64_t k64, int nf, int nl, Key key, int32_t* out) {
         for (int pass = 0; pass < 3; ++pass) {
             const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t digit = pass == 2 ? 1023u : 2047u;
-            s_hist[tid] = s_hist[tid + 1024] = 0;
+#pragma unroll
+            for (int b = 0; b < BINS; ++b) s_hist[b * THREADS + tid] = 0;
             __syncthreads();
 #pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += kPickChunk) {
-                if (n > kPickChunk) load(c0);
+            for (int c0 = 0; c0 < n; c0 += CHUNK) {
+                if (n > CHUNK) load(c0);
 #pragma unroll
-                for (int i = 0; i < kPickKeys; ++i) {
-                    const int t = c0 + i * kPickThreads + tid;
+                for (int i = 0; i < KEYS; ++i) {
+                    const int t = c0 + i * THREADS + tid;
                     if (t >= m0 && t < m1 && (u[i] & mask) == prefix) atomicAdd(&s_hist[(u[i] >> sh) & digit], 1u);
                 }
             }
             __syncthreads();
-            // the largest digit with at least `left` keys at or above it: thread t sums the bins 2047 - 2 t, 2046 - 2 t
-            const uint32_t hi = s_hist[2047 - 2 * tid], lo = s_hist[2046 - 2 * tid];
-            uint32_t incl = hi + lo;
+            // the largest digit with at least `left` keys at or above it; thread t has BINS bins, from the top
+            uint32_t h[BINS], sum = 0;
+#pragma unroll
+            for (int b = 0; b < BINS; ++b) {
+                h[b] = s_hist[2047 - BINS * tid - b];
+                sum += h[b];
+            }
+            uint32_t incl = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -167,56 +174,64 @@ TQ_DEVICE void pick(int n, int64_t k64, int nf, int nl, Key key, int32_t* out) {
             }
             if (lane == 31) s_warp[w] = incl;
             __syncthreads();
-            const uint32_t above = incl - hi - lo + __reduce_add_sync(0xffffffffu, lane < w ? s_warp[lane] : 0u);
-            if (above < left && above + hi + lo >= left) {
-                const bool first = above + hi >= left;
-                s_digit = 2047 - 2 * tid - (first ? 0 : 1);
-                s_left = left - above - (first ? 0 : hi);
+            uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < w && lane < NW ? s_warp[lane] : 0u);
+            if (above < left && above + sum >= left) {
+#pragma unroll
+                for (int b = 0; b < BINS; ++b) {
+                    if (above < left && above + h[b] >= left) {
+                        s_digit = 2047 - BINS * tid - b;
+                        s_left = left - above;
+                        s_here = h[b];
+                    }
+                    above += h[b];
+                }
             }
             __syncthreads();
             prefix |= s_digit << sh;
             mask |= digit << sh;
             left = s_left;
+            if (s_here == left) break;               // every key with these digits is taken: the others do not matter
         }
     }
-    // What lies above prefix is taken, and the first `left` of what equals it: an index's place is the number
-    // taken for sure before it plus the number of ties before it, up to `left`.
+    // What lies above prefix in the digits looked at is taken, and the first `left` of what equals it: an index's place is
+    // the number taken for sure before it plus the number of ties before it, up to `left`.
     const uint32_t below = (1u << lane) - 1;
     uint32_t sure0 = 0, ties0 = 0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += kPickChunk) {
-        if (any && n > kPickChunk) load(c0);
+    for (int c0 = 0; c0 < n; c0 += CHUNK) {
+        if (any && n > CHUNK) load(c0);
         uint32_t is_sure = 0, is_tie = 0;            // a bit per key
 #pragma unroll
-        for (int i = 0; i < kPickKeys; ++i) {
-            const int t = c0 + i * kPickThreads + tid;
+        for (int i = 0; i < KEYS; ++i) {
+            const int t = c0 + i * THREADS + tid;
             const bool mid = any && t >= m0 && t < m1;
-            const bool sure = t < n && (t < m0 || t >= m1 || (mid && u[i] > prefix)), tie = mid && u[i] == prefix;
+            const uint32_t v = u[i] & mask;
+            const bool sure = t < n && (t < m0 || t >= m1 || (mid && v > prefix)), tie = mid && v == prefix;
             const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
             if (lane == 0) s_cnt[i][w] = __popc(bs) | __popc(bt) << 16;
             is_sure |= (uint32_t)sure << i;
             is_tie |= (uint32_t)tie << i;
         }
         __syncthreads();
-        if (w < kPickKeys) {
-            const uint32_t v = s_cnt[w][lane];
+        for (int i = w; i < KEYS; i += NW) {
+            const uint32_t v = lane < NW ? s_cnt[i][lane] : 0u;
             uint32_t incl = v;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
+            for (int o = 1; o < NW; o <<= 1) {
                 const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += x;
             }
-            s_cnt[w][lane] = incl - v;
-            if (lane == 31) s_tot[w] = incl;
+            if (lane < NW) s_cnt[i][lane] = incl - v;
+            if (lane == NW - 1) s_tot[i] = incl;
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPickKeys; ++i) {
+        for (int i = 0; i < KEYS; ++i) {
             const bool sure = is_sure >> i & 1u, tie = is_tie >> i & 1u;
             const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
             const uint32_t c = s_cnt[i][w], ties = ties0 + (c >> 16) + __popc(bt & below);
             if (sure || (tie && ties < left))
-                out[sure0 + (c & 0xffffu) + __popc(bs & below) + min(ties, left)] = c0 + i * kPickThreads + tid;
+                out[sure0 + (c & 0xffffu) + __popc(bs & below) + min(ties, left)] = c0 + i * THREADS + tid;
             sure0 += s_tot[i] & 0xffffu;
             ties0 += s_tot[i] >> 16;
         }
@@ -233,18 +248,24 @@ struct WeightKey {
     TQ_DEVICE uint32_t operator()(int t) const { return __float_as_uint(fmaxf(acc[t], 0.f) + 0.f); }
 };
 
-__global__ void __launch_bounds__(kPickThreads) k_b8_pick_blocks(const __grid_constant__ B8SelectParams p) {
-    const int64_t row = blockIdx.x, si = row / p.c.n_kv, s = si / p.n_q;
-    const int nb = candidates(b8_len(p.c, s), p.n_q, (int)(si - s * p.n_q));
-    pick(nb, p.n_sel, p.n_first, p.n_last, ScoreKey{p.key + row * p.c.max_blocks}, p.sel + row * p.n_sel);
+template <int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS) k_b8_pick_blocks(const __grid_constant__ B8SelectParams p) {
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
+    const int row = blockIdx.x, si = row / p.c.n_kv, s = p.n_q == 1 ? si : si / p.n_q;
+    const int nb = candidates(b8_len(p.c, s), p.n_q, si - s * p.n_q);
+    pick<THREADS, KEYS>(nb, p.n_sel, p.n_first, p.n_last, ScoreKey{p.key + row * p.c.max_blocks},
+                        p.sel + (int64_t)row * p.n_sel);
 }
 
-__global__ void __launch_bounds__(kPickThreads) k_b8_pick_tokens(const __grid_constant__ B8EvictParams p) {
-    const int64_t row = blockIdx.x, s = row / p.c.n_kv;
-    const int n = b8_len(p.c, s) & ~31;
+template <int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS) k_b8_pick_tokens(const __grid_constant__ B8EvictParams p) {
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
+    const int row = blockIdx.x, s = row / p.c.n_kv, n = b8_len(p.c, s) & ~31;
     // (n_first and n_last are at most the tokens kept, and matter where there are more than those)
-    pick(n, 32 * p.keep_blocks, (int)p.n_first, (int)p.n_last, WeightKey{p.acc + row * p.c.max_blocks * 32},
-         p.kept + row * 32 * p.keep_blocks);
+    pick<THREADS, KEYS>(n, 32 * p.keep_blocks, (int)p.n_first, (int)p.n_last,
+                        WeightKey{p.acc + row * p.c.max_blocks * 32}, p.kept + row * 32 * p.keep_blocks);
 }
 
 // max(|c|) over the bytes c + 128 of a word, in the larger of two 16-bit halves: lo and hi run over words
@@ -270,6 +291,8 @@ template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_constant__ B8EvictParams p) {
     constexpr int CH = D / 16, TPI = 32 / CH, IT = CH;   // 16-byte chunks of a row; tokens per step; steps
     const B8Cache& c = p.c;
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
     const int lane = threadIdx.x & 31;
     int64_t id = (int64_t)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
     const int h = (int)(id % c.n_kv);
@@ -378,25 +401,29 @@ cudaError_t b8_launch_select(const B8SelectParams& p, cudaStream_t st) {
     const int64_t rows = p.c.n_seq * p.n_q * p.c.n_kv;
     const int64_t tiles = (p.c.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
     if (rows * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)(rows * tiles);
-    if (p.c.D == 64) k_b8_score<64><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
-    else if (p.c.D == 128) k_b8_score<128><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
-    else k_b8_score<256><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)tiles);
-    cudaError_t e = cudaGetLastError();
+    const dim3 grid((unsigned)(rows * tiles)), block(kScoreWarps * 32);
+    const cudaError_t e = tq_launch_pdl(p.c.D == 64    ? k_b8_score<64>
+                                        : p.c.D == 128 ? k_b8_score<128>
+                                                       : k_b8_score<256>,
+                                        grid, block, 0, st, p, (int)tiles);
     if (e != cudaSuccess) return e;
-    k_b8_pick_blocks<<<(unsigned)rows, kPickThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    // the fewest threads whose registers hold a whole row: many rows fit an SM, and little code runs
+    const dim3 r((unsigned)rows);
+    if (p.c.max_blocks <= 1024) return tq_launch_pdl(k_b8_pick_blocks<256, 4>, r, dim3(256), 0, st, p);
+    if (p.c.max_blocks <= 4096) return tq_launch_pdl(k_b8_pick_blocks<512, 8>, r, dim3(512), 0, st, p);
+    return tq_launch_pdl(k_b8_pick_blocks<1024, 16>, r, dim3(1024), 0, st, p);
 }
 
 cudaError_t b8_launch_evict(const B8EvictParams& p, cudaStream_t st) {
     const int64_t rows = p.c.n_seq * p.c.n_kv;
     const int64_t grid = (rows * 2 * (p.keep_blocks + 1) + kMoveWarps - 1) / kMoveWarps;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    k_b8_pick_tokens<<<(unsigned)rows, kPickThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const dim3 r((unsigned)rows);
+    const int64_t most = p.c.max_blocks * 32;
+    const cudaError_t e = most <= 1024   ? tq_launch_pdl(k_b8_pick_tokens<256, 4>, r, dim3(256), 0, st, p)
+                          : most <= 4096 ? tq_launch_pdl(k_b8_pick_tokens<512, 8>, r, dim3(512), 0, st, p)
+                                         : tq_launch_pdl(k_b8_pick_tokens<1024, 16>, r, dim3(1024), 0, st, p);
     if (e != cudaSuccess) return e;
-    if (p.c.D == 64) k_b8_move<64><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
-    else if (p.c.D == 128) k_b8_move<128><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
-    else k_b8_move<256><<<(unsigned)grid, kMoveWarps * 32, 0, st>>>(p);
-    return cudaGetLastError();
+    return tq_launch_pdl(p.c.D == 64 ? k_b8_move<64> : p.c.D == 128 ? k_b8_move<128> : k_b8_move<256>,
+                         dim3((unsigned)grid), dim3(kMoveWarps * 32), 0, st, p);
 }
