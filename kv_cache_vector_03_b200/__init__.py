@@ -263,60 +263,79 @@ class Cache8:
 
     def __init__(self, d, pages, table, length, open_):
         import torch
-        if open_.dim() != 5 or tuple(open_.shape[2:]) != (2, TQ_B8_BLOCK, d):
+        self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
+        self.dtypes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16}
+        self.getters = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if open_.dim() != 5 or open_.shape[2:] != (2, TQ_B8_BLOCK, d):
             raise ValueError(f"open_ is [n_seq, n_kv, 2, {TQ_B8_BLOCK}, {d}]: got {tuple(open_.shape)}")
         n_seq, n_kv = open_.shape[:2]
         nbytes = lib.tq_b8_page_bytes(d, n_kv)
         if nbytes == 0:
             raise TQError("tq_b8_page_bytes", TQ_ERR_UNSUPPORTED)
-        self.d, self.n_kv, self.n_seq, self.device = d, n_kv, n_seq, pages.device
         if pages.dim() != 2 or table.dim() != 2:
             raise ValueError("pages is [n_pages, page bytes], table is [n_seq, max_blocks]")
-        self.max_blocks = table.shape[1]
-        _tensor(self, "pages", pages, torch.uint8, (pages.shape[0], nbytes))
-        _tensor(self, "table", table, torch.int32, (n_seq, table.shape[1]))
-        _tensor(self, "length", length, torch.int32, (n_seq,))
-        _tensor(self, "open_", open_, torch.bfloat16, (n_seq, n_kv, 2, TQ_B8_BLOCK, d))
+        self.d, self.n_kv, self.n_seq, self.max_blocks = d, n_kv, n_seq, table.shape[1]
+        self.index = pages.get_device()           # -1 on the CPU, where no call is made
+        self.row = (n_seq, n_kv, TQ_B8_BLOCK * self.max_blocks)
+        self.c = tq_b8_cache(d, n_kv, n_seq, pages.shape[0], self.max_blocks,
+                             _tensor(self, "pages", pages, torch.uint8, (pages.shape[0], nbytes)),
+                             _tensor(self, "table", table, torch.int32, (n_seq, self.max_blocks)),
+                             _tensor(self, "length", length, torch.int32, (n_seq,)),
+                             _tensor(self, "open_", open_, torch.bfloat16, open_.shape))
         self.pages, self.table, self.length, self.open_ = pages, table, length, open_
-        self.c = tq_b8_cache(d, n_kv, n_seq, pages.shape[0], table.shape[1], pages.data_ptr(), table.data_ptr(),
-                             length.data_ptr(), open_.data_ptr())
         self.ref = ctypes.byref(self.c)
 
 
 def _tensor(cache, name, t, dtype, shape):
     """t's address, after the checks that a wrong tensor would fail silently."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is wanted")
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    return t.data_ptr()
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} is on device {t.get_device()}, the cache on {cache.index}")
+    raise ValueError(f"{name}: a contiguous tensor is wanted")
 
 
-def _b8_call(name, cache, ws, stream, *args):
-    """Enqueues lib.<name>(cache, *args, ws, stream) on the cache's GPU."""
-    import torch
-    if ws.device != cache.device:
-        raise ValueError(f"ws is on {ws.device}, the cache on {cache.device}")
-    dev = cache.device.index
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    here = torch._C._cuda_getDevice()
-    if here == dev:
-        return _check(name, getattr(lib, name)(cache.ref, *args, ws.data_ptr(), ws.numel(), handle))
-    with torch.cuda.device(dev):
-        return _check(name, getattr(lib, name)(cache.ref, *args, ws.data_ptr(), ws.numel(), handle))
+def _b8_dtype(cache, t):
+    dt = cache.dtypes.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return dt
+
+
+def _b8_call(name, fn, cache, ws, stream, *args):
+    """Enqueues fn(cache, *args, ws, stream) on the cache's GPU."""
+    dev = cache.index
+    if dev < 0 or ws.get_device() != dev or ws.dtype is not cache.u8 or not ws.is_contiguous():
+        raise ValueError(f"ws is a contiguous uint8 tensor on the cache's GPU ({dev}): got {ws.dtype} on {ws.device}")
+    raw, here = cache.getters
+    if stream is None:
+        stream = raw(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the cache on GPU {dev}")
+        stream = stream.cuda_stream
+    if here() == dev:
+        st = fn(cache.ref, *args, ws.data_ptr(), ws.numel(), stream)
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            st = fn(cache.ref, *args, ws.data_ptr(), ws.numel(), stream)
+    if st != TQ_OK:
+        raise TQError(name, st)
+    return st
 
 
 def _queries(cache, q):
-    if q.dim() != 4 or q.shape[2] % cache.n_kv:
-        raise ValueError(f"q is [n_seq, n_q, n_kv * g, d] with n_kv = {cache.n_kv}: got {tuple(q.shape)}")
-    n_q, g = q.shape[1], q.shape[2] // cache.n_kv
-    return _tensor(cache, "q", q, q.dtype, (cache.n_seq, n_q, cache.n_kv * g, cache.d)), _dtype(q), n_q, g
+    shape = q.shape
+    if len(shape) != 4 or shape[2] % cache.n_kv:
+        raise ValueError(f"q is [n_seq, n_q, n_kv * g, d] with n_kv = {cache.n_kv}: got {tuple(shape)}")
+    n_q, n_h = shape[1], shape[2]
+    return (_tensor(cache, "q", q, q.dtype, (cache.n_seq, n_q, n_h, cache.d)), _b8_dtype(cache, q), n_q,
+            n_h // cache.n_kv)
 
 
 def tq_b8_workspace_bytes(cache, n_q=0, g=0, n_sel=0, weights=True):
@@ -328,64 +347,64 @@ def tq_b8_workspace_bytes(cache, n_q=0, g=0, n_sel=0, weights=True):
 
 def tq_b8_append(cache, k, v, ws, add=None, stream=None):
     """k, v [n_seq, n_new, n_kv, d] (views with other sequence and token strides too); cache.length counts them."""
-    import torch
-    shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d)
-    for name, t in (("k", k), ("v", v)):
-        if t.dim() != 4 or tuple(t.shape) != shape or t.dtype != k.dtype:
-            raise ValueError(f"{name}: shape {shape} and {k.dtype} wanted, got {tuple(t.shape)} and {t.dtype}")
-        if t.device != cache.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-        st = t.stride()
-        if t.numel() and ((cache.d > 1 and st[3] != 1) or (cache.n_kv > 1 and st[2] != cache.d)):
-            raise ValueError(f"{name}: heads and channels lie next to each other, got strides {st}")
+    n_seq, n_kv, d, dev = cache.n_seq, cache.n_kv, cache.d, cache.index
+    n_new = k.shape[1] if k.dim() == 4 else -1
+    shape = (n_seq, n_new, n_kv, d)
+    if not (k.shape == shape and v.shape == shape and k.dtype is v.dtype):
+        raise ValueError(f"k, v: shape {shape} and one type wanted, got {tuple(k.shape)} and {tuple(v.shape)}, "
+                         f"{k.dtype} and {v.dtype}")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v are on devices {k.get_device()} and {v.get_device()}, the cache on {dev}")
     ks, vs = k.stride(), v.stride()
-    seq = [st[0] if cache.n_seq > 1 else 0 for st in (ks, vs)]
-    tok = [st[1] if shape[1] > 1 else 0 for st in (ks, vs)]
-    if seq[0] != seq[1] or tok[0] != tok[1]:
+    if n_new and n_seq and (ks[3] != 1 or vs[3] != 1 or (n_kv > 1 and (ks[2] != d or vs[2] != d))):
+        raise ValueError(f"k, v: heads and channels lie next to each other, got strides {ks} and {vs}")
+    seq, tok = (ks[0] if n_seq > 1 else 0), (ks[1] if n_new > 1 else 0)
+    if ks != vs and ((n_seq > 1 and vs[0] != seq) or (n_new > 1 and vs[1] != tok)):
         raise ValueError(f"k and v have other strides: {ks}, {vs}")
-    counts = None if add is None else _tensor(cache, "add", add, torch.int32, (cache.n_seq,))
-    return _b8_call("tq_b8_append", cache, ws, stream, k.data_ptr(), v.data_ptr(), _dtype(k), shape[1], seq[0], tok[0],
-                    counts)
+    counts = None if add is None else _tensor(cache, "add", add, cache.i32, (cache.n_seq,))
+    return _b8_call("tq_b8_append", lib.tq_b8_append, cache, ws, stream, k.data_ptr(), v.data_ptr(),
+                    _b8_dtype(cache, k), n_new, seq, tok, counts)
 
 
 def tq_b8_read(cache, k, v, ws, stream=None):
     """The last n_tok tokens of every sequence into k, v [n_seq, n_tok, n_kv, d] (fp32 or bf16)."""
     shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d)
-    kp, vp = _tensor(cache, "k", k, k.dtype, shape), _tensor(cache, "v", v, k.dtype, shape)
-    return _b8_call("tq_b8_read", cache, ws, stream, shape[1], kp, vp, _dtype(k))
+    return _b8_call("tq_b8_read", lib.tq_b8_read, cache, ws, stream, shape[1], _tensor(cache, "k", k, k.dtype, shape),
+                    _tensor(cache, "v", v, k.dtype, shape), _b8_dtype(cache, k))
 
 
 def tq_b8_attention(cache, q, scale, out, ws, sel=None, acc_in=None, acc_out=None, decay=1.0, stream=None):
-    import torch
+    """q [n_seq, n_q, n_kv * g, d] fp32 or bf16 -> out (fp32, the same shape); sel from tq_b8_select; acc_in and
+    acc_out fp32 [n_seq, n_kv, 32 * max_blocks]: the accumulated attention weights that tq_b8_evict goes by."""
     qp, dt, n_q, g = _queries(cache, q)
-    op = _tensor(cache, "out", out, torch.float32, q.shape)
-    sp, n_sel = None, 0
+    op = _tensor(cache, "out", out, cache.f32, q.shape)
+    sp, n_sel, ip, ap = None, 0, None, None
     if sel is not None:
         n_sel = sel.shape[-1]
-        sp = _tensor(cache, "sel", sel, torch.int32, (cache.n_seq, n_q, cache.n_kv, n_sel))
-    row = (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * cache.max_blocks)
-    ip = None if acc_in is None else _tensor(cache, "acc_in", acc_in, torch.float32, row)
-    ap = None if acc_out is None else _tensor(cache, "acc_out", acc_out, torch.float32, row)
-    return _b8_call("tq_b8_attention", cache, ws, stream, qp, dt, n_q, g, scale, sp, n_sel, ip, ap, decay, op)
+        sp = _tensor(cache, "sel", sel, cache.i32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+    if acc_in is not None:
+        ip = _tensor(cache, "acc_in", acc_in, cache.f32, cache.row)
+    if acc_out is not None:
+        ap = _tensor(cache, "acc_out", acc_out, cache.f32, cache.row)
+    return _b8_call("tq_b8_attention", lib.tq_b8_attention, cache, ws, stream, qp, dt, n_q, g, scale, sp, n_sel, ip, ap,
+                    decay, op)
 
 
 def tq_b8_select(cache, q, sel, ws, n_first=1, n_last=1, stream=None):
     """Fills sel int32 [n_seq, n_q, n_kv, n_sel] with the blocks tq_b8_attention is to look at."""
-    import torch
     qp, dt, n_q, g = _queries(cache, q)
     n_sel = sel.shape[-1]
-    sp = _tensor(cache, "sel", sel, torch.int32, (cache.n_seq, n_q, cache.n_kv, n_sel))
-    return _b8_call("tq_b8_select", cache, ws, stream, qp, dt, n_q, g, n_first, n_last, n_sel, sp)
+    sp = _tensor(cache, "sel", sel, cache.i32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+    return _b8_call("tq_b8_select", lib.tq_b8_select, cache, ws, stream, qp, dt, n_q, g, n_first, n_last, n_sel, sp)
 
 
 def tq_b8_evict(cache, acc, keep_blocks, dst_table, kept, length_out, acc_out, ws, n_first=0, n_last=0, stream=None):
-    import torch
-    row = (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * cache.max_blocks)
-    ap, op = _tensor(cache, "acc", acc, torch.float32, row), _tensor(cache, "acc_out", acc_out, torch.float32, row)
-    dp = _tensor(cache, "dst_table", dst_table, torch.int32, (cache.n_seq, cache.max_blocks))
-    kp = _tensor(cache, "kept", kept, torch.int32, (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * keep_blocks))
-    lp = _tensor(cache, "length_out", length_out, torch.int32, (cache.n_seq,))
-    return _b8_call("tq_b8_evict", cache, ws, stream, ap, keep_blocks, n_first, n_last, dp, kp, lp, op)
+    """Keeps 32 * keep_blocks of each sequence's paged tokens; dst_table and length_out are the cache afterwards."""
+    ap, op = _tensor(cache, "acc", acc, cache.f32, cache.row), _tensor(cache, "acc_out", acc_out, cache.f32, cache.row)
+    dp = _tensor(cache, "dst_table", dst_table, cache.i32, (cache.n_seq, cache.max_blocks))
+    kp = _tensor(cache, "kept", kept, cache.i32, (cache.n_seq, cache.n_kv, TQ_B8_BLOCK * keep_blocks))
+    lp = _tensor(cache, "length_out", length_out, cache.i32, (cache.n_seq,))
+    return _b8_call("tq_b8_evict", lib.tq_b8_evict, cache, ws, stream, ap, keep_blocks, n_first, n_last, dp, kp, lp, op)
 
 
 def tq_dequantize(codec: Codec, packed, n_streams, n_tok, out, ws=None, stream=None):
