@@ -94,11 +94,12 @@ TQ_DEVICE uint32_t atomic_add_acq_rel(uint32_t* at, uint32_t v) {
 // ------------------------------------------------------------------------ the list of units
 // "virtual sequences": a sequence, or with a selection one query token of it. The host has checked that
 // all units together, and the units of one virtual sequence over all heads and tiles, count below 2^30.
+template <bool SP>
 TQ_DEVICE int virt_units(const B8AttnParams& p, int v, int& n) {
-    const int s = p.sel && p.n_q > 1 ? v / p.n_q : v;
+    const int s = SP && p.n_q > 1 ? v / p.n_q : v;
     n = b8_len(p.c, s);
     const int open = ((n & 31) + 15) / 16;
-    if (!p.sel) return (n >> 5) + open;
+    if (!SP) return (n >> 5) + open;
     return n - p.n_q + (v - s * p.n_q) < 0 ? 0 : p.n_sel + open;
 }
 struct Plan {
@@ -119,18 +120,25 @@ struct Plan {
 //     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
 //     everyone would wait for it;
 //   else equal shares, cut where they fall.
-template <int THREADS>
+// Up to 32 virtual sequences: every warp for itself, a lane each; more: the block, a thread each, tile by tile.
+template <int THREADS, bool SP>
 TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) {
     constexpr int NW = THREADS / 32;
     __shared__ int s_sum[NW], s_max[NW], s_at[2][3];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int all;                                         // the sum over the block
+    const bool small = n_virt <= 32;
+    const int me = small ? lane : (int)threadIdx.x;
+    int all;                                         // the sum over the tile
     auto scan = [&](int x) {                         // inclusive sum up to this thread
         int incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
+        }
+        if (small) {
+            all = __shfl_sync(0xffffffffu, incl, 31);
+            return incl;
         }
         __syncthreads();
         if (lane == 31) s_sum[w] = incl;
@@ -141,85 +149,100 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
     };
     auto units_of = [&](int v) {
         int n;
-        return v < n_virt ? virt_units(p, v, n) : 0;
+        return v < n_virt ? virt_units<SP>(p, v, n) : 0;
+    };
+    // the thread for which `mine` holds hands its values to all of its warp or block
+    auto hand = [&](bool mine, int k, int x, int y, int z) {
+        if (small) {
+            const uint32_t who = __ballot_sync(0xffffffffu, mine);
+            if (who) {
+                const int src = __ffs(who) - 1;
+                x = __shfl_sync(0xffffffffu, x, src);
+                y = __shfl_sync(0xffffffffu, y, src);
+                z = __shfl_sync(0xffffffffu, z, src);
+            }
+            return make_int3(x, y, z);
+        }
+        if (mine) {
+            s_at[k][0] = x;
+            s_at[k][1] = y;
+            s_at[k][2] = z;
+        }
+        __syncthreads();
+        return make_int3(s_at[k][0], s_at[k][1], s_at[k][2]);
     };
     int total = 0, longest = 0, units = 0, incl = 0;
 #pragma unroll 1
-    for (int v0 = 0; v0 < n_virt; v0 += THREADS) {
-        units = units_of(v0 + threadIdx.x);
+    for (int v0 = 0; v0 < n_virt; v0 += small ? 32 : THREADS) {
+        units = units_of(v0 + me);
         longest = max(longest, units);
         incl = scan(units * segs);
         total += all;
     }
     longest = (int)__reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) s_max[w] = longest;
     pl.u0 = pl.mine = 0;
     pl.c0 = -1;
     if (total == 0) return;
-    __syncthreads();
-    longest = (int)__reduce_max_sync(0xffffffffu, lane < NW ? s_max[lane] : 0);
+    if (!small) {
+        if (lane == 0) s_max[w] = longest;
+        __syncthreads();
+        longest = (int)__reduce_max_sync(0xffffffffu, lane < NW ? s_max[lane] : 0);
+    }
     const bool one = n_virt <= THREADS;              // units and incl are this thread's virtual sequence's
     const int n_segs = n_virt * segs;
     const bool whole = longest <= kWholeUnits ||
                        (n_segs > p.grid && (n_segs + p.grid - 1) / p.grid * longest <= total / p.grid + kStraddle);
-    if (!whole && n_segs <= p.grid) {                // (then n_virt <= THREADS)
+    if (!whole && n_segs <= p.grid && one) {
         // 1 + floor(units (grid - segments) / total) parts each are never more than the grid together
         const int spare = min(p.grid, total / kMinUnits) - n_segs;
         const int parts = units ? 1 + (spare > 0 ? (int)((uint32_t)units * (uint32_t)spare / (uint32_t)total) : 0) : 0;
         const int upto = scan(parts * segs), b = blockIdx.x;
-        const int most = __syncthreads_or(units > parts * (total / p.grid + kStraddle));
-        if (!most) {
+        const bool far = units > parts * (total / p.grid + kStraddle);
+        if (!(small ? __any_sync(0xffffffffu, far) : __syncthreads_or(far))) {
             if (b >= all) return;
-            if (upto - parts * segs <= b && b < upto) {
-                const int j = b - (upto - parts * segs), seg = j / parts, part = j - seg * parts;
-                const int wide = units / parts, extra = units - wide * parts;
-                s_at[0][0] = threadIdx.x;
-                s_at[0][1] = seg * units + part * wide + min(part, extra);
-                s_at[0][2] = wide + (part < extra ? 1 : 0);
-                s_at[1][0] = b - part;
-                s_at[1][1] = b - part + parts - 1;
-            }
-            __syncthreads();
-            pl.virt = s_at[0][0];
-            pl.x = s_at[0][1];
-            pl.mine = s_at[0][2];
-            pl.c0 = s_at[1][0];
-            pl.c1 = s_at[1][1];
+            const bool mine = upto - parts * segs <= b && b < upto;
+            const int pp = max(parts, 1), j = b - (upto - parts * segs), seg = j / pp, part = j - seg * pp;
+            const int wide = units / pp, extra = units - wide * pp;
+            const int3 x = hand(mine, 0, me, seg * units + part * wide + min(part, extra), wide + (part < extra ? 1 : 0));
+            const int3 y = hand(mine, 1, b - part, b - part + parts - 1, 0);
+            pl.virt = x.x;
+            pl.x = x.y;
+            pl.mine = x.z;
+            pl.c0 = y.x;
+            pl.c1 = y.y;
             return;
         }
     }
-    const int ctas = min(p.grid, whole ? min(total, n_virt * segs) : max(1, total / kMinUnits));
+    const int ctas = min(p.grid, whole ? min(total, n_segs) : max(1, total / kMinUnits));
     pl.base = total / ctas;
     pl.extra = total - pl.base * ctas;
     if ((int)blockIdx.x >= ctas) return;
     const int lo = pl.share(blockIdx.x), hi = pl.share(blockIdx.x + 1);
-    if (one) incl = scan(units * segs);
+    if (one) all = total;                            // (the tile's, again)
+    int3 start = make_int3(0, 0, 0), end = make_int3(0, 0, total);
 #pragma unroll 1
     for (int v0 = 0, base = 0;; v0 += THREADS) {
         if (!one) {
-            units = units_of(v0 + threadIdx.x);
+            units = units_of(v0 + me);
             incl = scan(units * segs);
         }
         const int before = base + incl - units * segs;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int u = k ? hi : lo;
-            if (before <= u && u < base + incl) {
-                int off = u - before;
-                if (whole) off -= off % units;
-                s_at[k][0] = v0 + threadIdx.x;
-                s_at[k][1] = off;
-                s_at[k][2] = before + off;
-            }
+            if (u < base || u >= base + all) continue;   // not in this tile
+            const bool mine = before <= u && u < base + incl;
+            int off = u - before;
+            if (whole && mine) off -= off % units;
+            (k ? end : start) = hand(mine, k, v0 + me, off, before + off);
         }
         base += all;
         if (base > hi || base >= total) break;
     }
-    __syncthreads();
-    pl.virt = s_at[0][0];
-    pl.x = s_at[0][1];
-    pl.u0 = s_at[0][2];
-    pl.mine = (hi < total ? s_at[1][2] : total) - pl.u0;
+    pl.virt = start.x;
+    pl.x = start.y;
+    pl.u0 = start.z;
+    pl.mine = end.z - pl.u0;
 }
 
 template <int D>
@@ -235,7 +258,7 @@ struct __align__(8) Record {
     int block;
 };
 
-template <int D, int NT, bool WT>
+template <int D, int NT, bool WT, bool SP>
 __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_attn(const __grid_constant__ B8AttnParams p) {
     using Sh = Shape<D, NT>;
     constexpr int NW = Sh::warps, ST = Sh::stages, SB = Sh::stage_bytes, RD = Sh::rounds;
@@ -263,19 +286,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     tq_pdl_wait();                                   // nothing is read before the kernel in front is done
 
     const int segs = c.n_kv * p.row_tiles;
-    const int n_virt = (int)(p.sel ? c.n_seq * p.n_q : c.n_seq);
-    const int rows = p.sel ? p.g : p.n_q * p.g;      // query rows of a virtual sequence and kv head
+    const int n_virt = (int)(SP ? c.n_seq * p.n_q : c.n_seq);
+    const int rows = SP ? p.g : p.n_q * p.g;      // query rows of a virtual sequence and kv head
     auto q_row = [&](int v, int h, int r) {
-        const int t = p.sel ? 0 : r / p.g;           // query token within the virtual sequence
-        return ((int64_t)v * (p.sel ? 1 : p.n_q) + t) * c.n_kv * p.g + h * p.g + r - t * p.g;
+        const int t = SP ? 0 : r / p.g;           // query token within the virtual sequence
+        return ((int64_t)v * (SP ? 1 : p.n_q) + t) * c.n_kv * p.g + h * p.g + r - t * p.g;
     };
     Plan pl;
-    make_plan<NW * 32>(p, n_virt, segs, pl);
+    make_plan<NW * 32, SP>(p, n_virt, segs, pl);
     // rows of sequences without a token are zeros
 #pragma unroll 1
     for (int v = blockIdx.x; v < n_virt; v += gridDim.x) {
         int n;
-        if (virt_units(p, v, n) == 0) {
+        if (virt_units<SP>(p, v, n) == 0) {
 #pragma unroll 1
             for (int hr = w; hr < c.n_kv * rows; hr += NW) {
                 float* out = p.out + q_row(v, hr / rows, hr % rows) * c.d;
@@ -299,17 +322,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         if (fi < mine) {
             int n, units;
 #pragma unroll 1
-            while (fx >= (units = virt_units(p, fv, n)) * segs) {
+            while (fx >= (units = virt_units<SP>(p, fv, n)) * segs && fv + 1 < n_virt) {
                 fx -= units * segs;
                 ++fv;
             }
-            const int seg = fx / units, off = fx - seg * units, pages = p.sel ? p.n_sel : n >> 5;
-            const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, s = p.sel && p.n_q > 1 ? fv / p.n_q : fv;
+            const int seg = fx / units, off = fx - seg * units, pages = SP ? p.n_sel : n >> 5;
+            const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, s = SP && p.n_q > 1 ? fv / p.n_q : fv;
             if (off >= pages) {
                 const uint16_t* k = b8_open(c, s, h, 0) + 16 * (off - pages) * c.d;
                 r = {reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(k + 32 * c.d), -2 - (off - pages), n >> 5};
             } else {
-                r.block = p.sel ? p.sel[((int64_t)fv * c.n_kv + h) * p.n_sel + off] : off;
+                r.block = SP ? p.sel[((int64_t)fv * c.n_kv + h) * p.n_sel + off] : off;
                 if (r.block >= 0 && r.block < (n >> 5)) {
                     const uint8_t* page = b8_page(c, c.table[(int64_t)s * c.max_blocks + r.block]);
                     if (page) r = {page + c.header_bytes + (size_t)h * (64 * D), page + (size_t)h * (32 + 2 * D), 0, r.block};
@@ -358,15 +381,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     for (int u = 0; u < mine;) {
         int n, units;
 #pragma unroll 1
-        while (x0 >= (units = virt_units(p, v, n)) * segs) {
+        while (x0 >= (units = virt_units<SP>(p, v, n)) * segs && v + 1 < n_virt) {
             x0 -= units * segs;
             ++v;
         }
         const int seg = x0 / units, off = x0 - seg * units;
         const int part = min(units - off, mine - u);
         const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * 8 * NT;
-        const int s = p.sel && p.n_q > 1 ? v / p.n_q : v;
-        const int all_see = n - p.n_q + (p.sel ? v - s * p.n_q : 0);          // every row sees the positions up to here
+        const int s = SP && p.n_q > 1 ? v / p.n_q : v;
+        const int all_see = n - p.n_q + (SP ? v - s * p.n_q : 0);          // every row sees the positions up to here
 
         if (u == 0) {
 #pragma unroll 1
@@ -444,7 +467,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sees[nt][e] = p.sel ? all_see : all_see + (row0 + 8 * nt + 2 * tq + e) / p.g;
+            for (int e = 0; e < 2; ++e) sees[nt][e] = SP ? all_see : all_see + (row0 + 8 * nt + 2 * tq + e) / p.g;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -460,7 +483,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             const int what = ok ? s_meta[st].x : -1, b = ok ? s_meta[st].y : 0;
             float* lg = nullptr;                          // this unit's logits, [row][logit_row], if they are wanted
             if (WT) {
-                const int at = off + i - u, pages = p.sel ? p.n_sel : n >> 5;
+                const int at = off + i - u, pages = SP ? p.n_sel : n >> 5;
                 lg = p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0) * p.logit_row +
                      (at < pages ? 32 * (int64_t)at : 32 * (int64_t)pages + 16 * (at - pages));
             }
@@ -979,17 +1002,18 @@ __global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8At
     p.acc_out[at] = a;
 }
 
-template <int D, int NT, bool WT>
+template <int D, int NT, bool WT, bool SP>
 cudaError_t launch_one(const B8AttnParams& p, cudaStream_t st) {
     using Sh = Shape<D, NT>;
     static TqLaunchCache cache;
-    const cudaError_t e = tq_kernel_setup(k_b8_attn<D, NT, WT>, Sh::warps * 32, Sh::smem, cache, nullptr, nullptr);
+    const cudaError_t e = tq_kernel_setup(k_b8_attn<D, NT, WT, SP>, Sh::warps * 32, Sh::smem, cache, nullptr, nullptr);
     if (e != cudaSuccess) return e;
-    return tq_launch_pdl(k_b8_attn<D, NT, WT>, dim3((unsigned)p.grid), dim3(Sh::warps * 32), Sh::smem, st, p);
+    return tq_launch_pdl(k_b8_attn<D, NT, WT, SP>, dim3((unsigned)p.grid), dim3(Sh::warps * 32), Sh::smem, st, p);
 }
 template <int D, int NT>
 cudaError_t launch(const B8AttnParams& p, cudaStream_t st) {
-    return p.acc_out ? launch_one<D, NT, true>(p, st) : launch_one<D, NT, false>(p, st);
+    if (p.sel) return p.acc_out ? launch_one<D, NT, true, true>(p, st) : launch_one<D, NT, false, true>(p, st);
+    return p.acc_out ? launch_one<D, NT, true, false>(p, st) : launch_one<D, NT, false, false>(p, st);
 }
 
 }  // namespace

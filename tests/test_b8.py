@@ -370,6 +370,7 @@ CASES = [  # d, n_kv, g, n_q, lengths, dtype
     (128, 8, 4, 1, [500], "bf16"), (128, 2, 1, 1, [1, 0, 31, 32, 33], "bf16"), (128, 2, 8, 1, [257, 64, 1000], "f32"),
     (64, 3, 3, 2, [0, 1, 2, 33, 96], "f32"), (64, 1, 7, 5, [3, 64, 66, 290], "bf16"), (40, 2, 5, 3, [70, 5], "bf16"),
     (8, 1, 2, 1, [40], "f32"), (200, 2, 4, 1, [100, 45], "bf16"), (256, 1, 8, 2, [129, 31], "f32"),
+    (64, 4, 6, 4, [160 + (977 + 40503 * s) % 1140 for s in range(24)], "f32"),
     (128, 1, 16, 3, [320], "bf16"), (96, 1, 33, 1, [77], "f32"), (128, 1, 2, 40, [37, 64, 200], "bf16")]
 
 
@@ -410,6 +411,31 @@ def test_attention(m, d, n_kv, g, n_q, lens, dtype):
         sums = weight.copy()
         sums[:, :old] += 0.75 * a[:, :old]
         assert np.all(np.abs(w[:, :n] - sums) <= rel * sums + 1e-30) and (w[:, n:] == 99.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,n_seq,long", [(256, 200, 1100), (64, 300, 1100), (64, 300, 40), (128, 40, 1500), (128, 3, 6000)])
+def test_attention_many_ragged_sequences(m, d, n_seq, long):
+    """Batches of more sequences than a warp, a block or the grid has members, with few long ones among short
+    and empty ones, so that work is cut within and between sequences; the same bits every time."""
+    import torch
+    lens = [(7 * s) % 45 for s in range(n_seq)]
+    for s in (0, n_seq // 2, n_seq - 1):
+        lens[s] = long - s % 7
+    p = Pair(m, d, 1, n_seq, -(-long // 32) + 1, 40 + d)
+    p.append(lens)
+    q, q64 = p.queries(1, 3, "bf16")
+    ws = p.workspace(1, 3)
+    out, again = torch.full(q.shape, float("nan"), device="cuda"), torch.empty(q.shape, device="cuda")
+    m.tq_b8_attention(p.cache, q, 0.1, out, ws)
+    for _ in range(3):
+        m.tq_b8_attention(p.cache, q, 0.1, again, ws)
+        assert torch.equal(out, again)
+    assert p.ok(ws)
+    got = out.double().cpu().numpy().reshape(q64.shape)
+    for s, sq in enumerate(p.seqs):
+        want, _, size, reach = ref.attention(sq, q64[s], 0.1)
+        close(got[s], want, size, reach, d)
 
 
 @pytest.mark.gpu
