@@ -20,11 +20,13 @@ constexpr int kReadWarps = 8;
 // 8 channels as bf16 pairs
 template <bool F32>
 TQ_DEVICE uint4 load8(const void* base, int64_t elem) {
-    if (!F32) return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-    const float4 a = f[0], b = f[1];
-    const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
-                                 __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
+    if (!F32) return tq_ldg_stream(static_cast<const uint16_t*>(base) + elem);
+    const uint4 a = tq_ldg_stream(static_cast<const float*>(base) + elem);
+    const uint4 b = tq_ldg_stream(static_cast<const float*>(base) + elem + 4);
+    const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(__uint_as_float(a.x), __uint_as_float(a.y)),
+                                 __floats2bfloat162_rn(__uint_as_float(a.z), __uint_as_float(a.w)),
+                                 __floats2bfloat162_rn(__uint_as_float(b.x), __uint_as_float(b.y)),
+                                 __floats2bfloat162_rn(__uint_as_float(b.z), __uint_as_float(b.w))};
     return *reinterpret_cast<const uint4*>(r);
 }
 

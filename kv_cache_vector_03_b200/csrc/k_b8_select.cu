@@ -282,14 +282,17 @@ struct ByteRange {
     }
 };
 
-// One warp per (sequence, new block, keys or values, head): gathers 32 kept tokens, finds the new
-// scale, requantizes by one multiply-add per code and writes the block, its scale and summary.
-// The warps of new block keep_blocks move what belongs to the open block: its acc, the length.
-// A lane holds 16 channels of D / 16 tokens; codes stay packed but for the multiply-add, maxima and the
-// summary's ranges are taken on 16-bit pairs.
+// One warp per (sequence, new block, head), keys and values together where the registers hold both (D <= 128): gathers
+// 32 kept tokens, finds the new scales, requantizes by one multiply-add per code and writes the block, its scales and
+// summary. The warps of new block keep_blocks move what belongs to the open block: its acc, the length.
+// What bounds it is the chain kept -> table -> rows: all rows of a warp are under way at once. A lane holds 16 channels
+// of D / 16 tokens; codes stay packed but for the multiply-add, maxima and the summary's ranges are taken on 16-bit pairs.
+template <int D>
+struct MoveSides { static constexpr int n = D == 256 ? 1 : 2; };
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_constant__ B8EvictParams p) {
     constexpr int CH = D / 16, TPI = 32 / CH, IT = CH;   // 16-byte chunks of a row; tokens per step; steps
+    constexpr int NS = MoveSides<D>::n;
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
@@ -297,101 +300,113 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
     int64_t id = (int64_t)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
     const int h = (int)(id % c.n_kv);
     id /= c.n_kv;
-    const int side = (int)(id & 1);
-    id >>= 1;
+    const int side0 = NS == 1 ? (int)(id & 1) : 0;
+    if (NS == 1) id >>= 1;
     const int64_t j = id % (p.keep_blocks + 1), s = id / (p.keep_blocks + 1);
     if (s >= c.n_seq) return;
     const int n = b8_len(c, s), nfull = n >> 5, r = n & 31;
     const int left = (int)min((int64_t)nfull, p.keep_blocks);
     const int64_t arow = (s * c.n_kv + h) * c.max_blocks * 32;
     if (j == p.keep_blocks) {
-        if (side == 0 && lane < r) p.acc_out[arow + 32 * left + lane] = p.acc[arow + 32 * nfull + lane];
-        if (side == 0 && h == 0 && lane == 0) p.len_out[s] = 32 * left + r;
+        if (side0 == 0 && lane < r) p.acc_out[arow + 32 * left + lane] = p.acc[arow + 32 * nfull + lane];
+        if (side0 == 0 && h == 0 && lane == 0) p.len_out[s] = 32 * left + r;
         return;
     }
     if (j >= left) return;
     const int tok = p.kept[((s * c.n_kv + h) * p.keep_blocks + j) * 32 + lane];
     uint8_t* page = b8_page(c, c.table[s * c.max_blocks + (tok >> 5)]);
     uint8_t* dst = b8_page(c, p.dst_table[s * c.max_blocks + j]);
-    const float sc = page ? *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side) : 0.f;
-    const uint8_t* row = page ? b8_codes(c, page, h, side) + (tok & 31) * D : nullptr;
+    float2 sc = make_float2(0.f, 0.f);                   // key and value scale of token `lane`
+    if (page) sc = *reinterpret_cast<const float2*>(b8_entry(c, page, h));
+    const uint8_t* row = page ? b8_codes(c, page, h, side0) + (tok & 31) * D : nullptr;
     const int ch = lane % CH, t0 = lane / CH;
-    uint4 x[IT];
+    uint4 x[NS][IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int t = t0 + i * TPI;
         const uint8_t* rp = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)row, t));
         const int tk = __shfl_sync(0xffffffffu, tok, t) & 31;
-        x[i] = rp ? tq_ldg_stream(rp + ((ch ^ b8_swz(tk, CH)) << 4))
-                  : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-    }
-    if (side == 0) p.acc_out[arow + 32 * j + lane] = p.acc[arow + tok];
-    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        ByteRange br = {0x00ff00ffu, 0u};
-        br.take(x[i].x);
-        br.take(x[i].y);
-        br.take(x[i].z);
-        br.take(x[i].w);
-        int m = br.top();
-#pragma unroll
-        for (int o = 1; o < CH; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        top = fmaxf(top, __fmul_rn(__fmul_rn((float)m, kB8Inv127), __shfl_sync(0xffffffffu, sc, t0 + i * TPI)));
+        for (int y = 0; y < NS; ++y)
+            x[y][i] = rp ? tq_ldg_stream(rp + y * 32 * D + ((ch ^ b8_swz(tk, CH)) << 4))
+                         : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
     }
-    top = tq_warp_max(top);
+    if (side0 == 0) p.acc_out[arow + 32 * j + lane] = p.acc[arow + tok];
+    float top[NS];
+#pragma unroll
+    for (int y = 0; y < NS; ++y) {
+        const float mine = (NS == 1 ? side0 : y) ? sc.y : sc.x;
+        top[y] = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            ByteRange br = {0x00ff00ffu, 0u};
+            br.take(x[y][i].x);
+            br.take(x[y][i].y);
+            br.take(x[y][i].z);
+            br.take(x[y][i].w);
+            int m = br.top();
+#pragma unroll
+            for (int o = 1; o < CH; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            top[y] = fmaxf(top[y], __fmul_rn(__fmul_rn((float)m, kB8Inv127), __shfl_sync(0xffffffffu, mine, t0 + i * TPI)));
+        }
+        top[y] = tq_warp_max(top[y]);
+    }
     if (!dst) return;
-    const float ratio = top > 0.f ? sc / top : 0.f;
-    uint8_t* drow = b8_codes(c, dst, h, side);
-    uint32_t lo[8], hi[8];                               // 16-bit ranges of this lane's 16 channels
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        lo[k] = 0x00ff00ffu;
-        hi[k] = 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int t = t0 + i * TPI;
-        const float rt = __shfl_sync(0xffffffffu, ratio, t);
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                f[k] = fmaf(__uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f, rt, kRound);
-            o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
-                               __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
-            if (side == 0) {
-                const uint32_t e = o[q] & 0x00ff00ffu, d = __byte_perm(o[q], 0, 0x4341);
-                lo[2 * q] = __vminu2(lo[2 * q], e);
-                hi[2 * q] = __vmaxu2(hi[2 * q], e);
-                lo[2 * q + 1] = __vminu2(lo[2 * q + 1], d);
-                hi[2 * q + 1] = __vmaxu2(hi[2 * q + 1], d);
-            }
-        }
-        *reinterpret_cast<uint4*>(drow + t * D + ((ch ^ b8_swz(t, CH)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
     uint8_t* e = b8_entry(c, dst, h);
-    if (lane == 0) *reinterpret_cast<float*>(e + 4 * side) = top;
-    if (side) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int y = 0; y < NS; ++y) {
+        const int side = NS == 1 ? side0 : y;
+        const float ratio = top[y] > 0.f ? (side ? sc.y : sc.x) / top[y] : 0.f;
+        uint8_t* drow = b8_codes(c, dst, h, side);
+        uint32_t lo[8], hi[8];                           // 16-bit ranges of this lane's 16 channels
 #pragma unroll
-        for (int o = CH; o < 32; o <<= 1) {
-            lo[k] = __vminu2(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
-            hi[k] = __vmaxu2(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+        for (int k = 0; k < 8; ++k) {
+            lo[k] = 0x00ff00ffu;
+            hi[k] = 0u;
         }
-    if (lane < CH) {
-        uint32_t l[4], g[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {                    // even bytes from one pair, odd bytes from the other
-            l[q] = (lo[2 * q] | lo[2 * q + 1] << 8) ^ 0x80808080u;
-            g[q] = (hi[2 * q] | hi[2 * q + 1] << 8) ^ 0x80808080u;
+        for (int i = 0; i < IT; ++i) {
+            const int t = t0 + i * TPI;
+            const float rt = __shfl_sync(0xffffffffu, ratio, t);
+            const uint32_t u[4] = {x[y][i].x, x[y][i].y, x[y][i].z, x[y][i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    f[k] = fmaf(__uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f, rt, kRound);
+                o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
+                                   __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
+                if (side == 0) {
+                    const uint32_t ev = o[q] & 0x00ff00ffu, od = __byte_perm(o[q], 0, 0x4341);
+                    lo[2 * q] = __vminu2(lo[2 * q], ev);
+                    hi[2 * q] = __vmaxu2(hi[2 * q], ev);
+                    lo[2 * q + 1] = __vminu2(lo[2 * q + 1], od);
+                    hi[2 * q + 1] = __vmaxu2(hi[2 * q + 1], od);
+                }
+            }
+            *reinterpret_cast<uint4*>(drow + t * D + ((ch ^ b8_swz(t, CH)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4*>(e + 32 + 16 * ch) = make_uint4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<uint4*>(e + 32 + D + 16 * ch) = make_uint4(g[0], g[1], g[2], g[3]);
+        if (lane == 0) *reinterpret_cast<float*>(e + 4 * side) = top[y];
+        if (side) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int o = CH; o < 32; o <<= 1) {
+                lo[k] = __vminu2(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+                hi[k] = __vmaxu2(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+            }
+        if (lane < CH) {
+            uint32_t l[4], g[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {                // even bytes from one pair, odd bytes from the other
+                l[q] = (lo[2 * q] | lo[2 * q + 1] << 8) ^ 0x80808080u;
+                g[q] = (hi[2 * q] | hi[2 * q + 1] << 8) ^ 0x80808080u;
+            }
+            *reinterpret_cast<uint4*>(e + 32 + 16 * ch) = make_uint4(l[0], l[1], l[2], l[3]);
+            *reinterpret_cast<uint4*>(e + 32 + D + 16 * ch) = make_uint4(g[0], g[1], g[2], g[3]);
+        }
     }
 }
 
@@ -416,7 +431,7 @@ cudaError_t b8_launch_select(const B8SelectParams& p, cudaStream_t st) {
 
 cudaError_t b8_launch_evict(const B8EvictParams& p, cudaStream_t st) {
     const int64_t rows = p.c.n_seq * p.c.n_kv;
-    const int64_t grid = (rows * 2 * (p.keep_blocks + 1) + kMoveWarps - 1) / kMoveWarps;
+    const int64_t grid = (rows * (p.c.D == 256 ? 2 : 1) * (p.keep_blocks + 1) + kMoveWarps - 1) / kMoveWarps;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 r((unsigned)rows);
     const int64_t most = p.c.max_blocks * 32;
