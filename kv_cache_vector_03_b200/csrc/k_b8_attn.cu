@@ -37,7 +37,7 @@ constexpr int kAccTok = 256;
 constexpr int kCtasPerSm = 2;
 template <int D, int NT>
 struct Shape {
-    static constexpr int warps = D == 256 ? 4 : NT == 2 && D == 128 ? 6 : 8;
+    static constexpr int warps = D == 256 || NT * D == 256 ? 4 : D == 128 ? 6 : 8;
     static constexpr int stages = D == 64 ? 20 : D == 128 ? 10 : 5;
     static constexpr int stage_bytes = 64 * D + 128;   // keys, values, scales
     static constexpr int rounds = NT * D == 64 ? 1 : NT * D == 128 ? 2 : D == 256 ? 2 : 4;
