@@ -29,6 +29,7 @@ constexpr float kBias = 7.f;         // weights are kept as 2^(7 + logit - m): t
 constexpr float kSlack = 8.f;        // m follows the maximum once it is passed by 2^8: 2^(7 + 8) < 65504
 constexpr int kMinUnits = 8;        // units a CTA takes at least, where segments are shared
 constexpr int kStraddle = 24;
+constexpr int kSegment = 10;         // what a segment costs beside its units, in units
 constexpr int kWholeUnits = 32;      // segments up to here are not shared
 constexpr int kAccTok = 256;
 
@@ -103,10 +104,11 @@ TQ_DEVICE int virt_units(const B8AttnParams& p, int v, int& n) {
     return n - p.n_q + (v - s * p.n_q) < 0 ? 0 : p.n_sel + open;
 }
 struct Plan {
-    int u0, mine;                // this CTA's units begin at u0 (counted over the whole list), mine of them
-    int virt, x;                 // u0 is unit x of virtual sequence virt
+    int mine;                    // how many units this CTA has,
+    int virt, x;                 // from unit x of virtual sequence virt on
     int c0, c1;                  // the CTAs that share this CTA's only segment, or c0 = -1: ask owner()
-    int base, extra;             // equal shares: base units, one more for the first `extra` CTAs
+    int before;                  // (then) the price of all virtual sequences before virt
+    int base, extra;             // equal shares: a price of base, one more for the first `extra` CTAs
     TQ_DEVICE int share(int c) const { return c * base + min(c, extra); }
     TQ_DEVICE int owner(int u) const {
         const int wide = extra * (base + 1);
@@ -119,12 +121,13 @@ struct Plan {
 //   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length. A CTA
 //     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
 //     everyone would wait for it;
-//   else equal shares, cut where they fall.
+//   else equal shares, cut where they fall. A segment is priced at its units and kSegment more, for what each begun
+//     segment costs (its queries, the meeting of the warps), so that CTAs with many segments get fewer units.
 // Up to 32 virtual sequences: every warp for itself, a lane each; more: the block, a thread each, tile by tile.
 template <int THREADS, bool SP>
 TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) {
     constexpr int NW = THREADS / 32;
-    __shared__ int s_sum[NW], s_max[NW], s_at[2][3];
+    __shared__ int s_sum[NW], s_max[NW], s_at[2][4];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const bool small = n_virt <= 32;
     const int me = small ? lane : (int)threadIdx.x;
@@ -152,7 +155,7 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
         return v < n_virt ? virt_units<SP>(p, v, n) : 0;
     };
     // the thread for which `mine` holds hands its values to all of its warp or block
-    auto hand = [&](bool mine, int k, int x, int y, int z) {
+    auto hand = [&](bool mine, int k, int x, int y, int z, int t) {
         if (small) {
             const uint32_t who = __ballot_sync(0xffffffffu, mine);
             if (who) {
@@ -160,27 +163,30 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
                 x = __shfl_sync(0xffffffffu, x, src);
                 y = __shfl_sync(0xffffffffu, y, src);
                 z = __shfl_sync(0xffffffffu, z, src);
+                t = __shfl_sync(0xffffffffu, t, src);
             }
-            return make_int3(x, y, z);
+            return make_int4(x, y, z, t);
         }
         if (mine) {
             s_at[k][0] = x;
             s_at[k][1] = y;
             s_at[k][2] = z;
+            s_at[k][3] = t;
         }
         __syncthreads();
-        return make_int3(s_at[k][0], s_at[k][1], s_at[k][2]);
+        return make_int4(s_at[k][0], s_at[k][1], s_at[k][2], s_at[k][3]);
     };
-    int total = 0, longest = 0, units = 0, incl = 0;
+    int total = 0, longest = 0, units = 0, incl = 0, filled = 0;   // filled: virtual sequences that have units
 #pragma unroll 1
     for (int v0 = 0; v0 < n_virt; v0 += small ? 32 : THREADS) {
         units = units_of(v0 + me);
         longest = max(longest, units);
         incl = scan(units * segs);
         total += all;
+        filled += small ? __popc(__ballot_sync(0xffffffffu, units > 0)) : __syncthreads_count(units > 0);
     }
     longest = (int)__reduce_max_sync(0xffffffffu, longest);
-    pl.u0 = pl.mine = 0;
+    pl.mine = 0;
     pl.c0 = -1;
     if (total == 0) return;
     if (!small) {
@@ -203,8 +209,8 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
             const bool mine = upto - parts * segs <= b && b < upto;
             const int pp = max(parts, 1), j = b - (upto - parts * segs), seg = j / pp, part = j - seg * pp;
             const int wide = units / pp, extra = units - wide * pp;
-            const int3 x = hand(mine, 0, me, seg * units + part * wide + min(part, extra), wide + (part < extra ? 1 : 0));
-            const int3 y = hand(mine, 1, b - part, b - part + parts - 1, 0);
+            const int4 x = hand(mine, 0, me, seg * units + part * wide + min(part, extra), wide + (part < extra ? 1 : 0), 0);
+            const int4 y = hand(mine, 1, b - part, b - part + parts - 1, 0, 0);
             pl.virt = x.x;
             pl.x = x.y;
             pl.mine = x.z;
@@ -214,35 +220,36 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
         }
     }
     const int ctas = min(p.grid, whole ? min(total, n_segs) : max(1, total / kMinUnits));
-    pl.base = total / ctas;
-    pl.extra = total - pl.base * ctas;
+    const int price = total + kSegment * segs * filled;
+    pl.base = price / ctas;
+    pl.extra = price - pl.base * ctas;
     if ((int)blockIdx.x >= ctas) return;
     const int lo = pl.share(blockIdx.x), hi = pl.share(blockIdx.x + 1);
-    if (one) all = total;                            // (the tile's, again)
-    int3 start = make_int3(0, 0, 0), end = make_int3(0, 0, total);
+    int4 start = make_int4(0, 0, 0, 0), end = make_int4(0, 0, total, 0);   // virtual sequence, its unit, units before, price before
 #pragma unroll 1
-    for (int v0 = 0, base = 0;; v0 += THREADS) {
+    for (int v0 = 0, base = 0, base_price = 0;; v0 += THREADS) {
         if (!one) {
             units = units_of(v0 + me);
             incl = scan(units * segs);
         }
-        const int before = base + incl - units * segs;
+        const int here = one ? total : all, mine = units ? units + kSegment : 0, upto = scan(mine * segs), first = upto - mine * segs;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int u = k ? hi : lo;
-            if (u < base || u >= base + all) continue;   // not in this tile
-            const bool mine = before <= u && u < base + incl;
-            int off = u - before;
-            if (whole && mine) off -= off % units;
-            (k ? end : start) = hand(mine, k, v0 + me, off, before + off);
+            const int u = (k ? hi : lo) - base_price;
+            if (u < 0 || u >= all) continue;             // not in this tile
+            const bool is = first <= u && u < upto;
+            const int seg = is ? (u - first) / mine : 0, off = is ? max(0, u - first - seg * mine - kSegment) : 0;
+            const int x = seg * units + (whole ? 0 : off);
+            (k ? end : start) = hand(is, k, v0 + me, x, base + incl - units * segs + x, base_price + first);
         }
-        base += all;
-        if (base > hi || base >= total) break;
+        base += here;
+        base_price += all;
+        if (base_price > hi || base_price >= price) break;
     }
     pl.virt = start.x;
     pl.x = start.y;
-    pl.u0 = start.z;
-    pl.mine = end.z - pl.u0;
+    pl.mine = end.z - start.z;
+    pl.before = start.w;
 }
 
 template <int D>
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         ++issued;
     };
 
-    int i = w, v = pl.virt, x0 = pl.x;               // i: this warp's next unit, in stage st
+    int i = w, v = pl.virt, x0 = pl.x, before = pl.before;   // i: this warp's next unit, in stage st
     int st = w % ST;
     uint32_t phase = 0;
     // where a lane's values (tokens 2 tq, 2 tq + 1) lie in a page; 8 tokens on is 8 D on
@@ -383,6 +390,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll 1
         while (x0 >= (units = virt_units<SP>(p, v, n)) * segs && v + 1 < n_virt) {
             x0 -= units * segs;
+            before += units ? (units + kSegment) * segs : 0;
             ++v;
         }
         const int seg = x0 / units, off = x0 - seg * units;
@@ -892,7 +900,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         if (!whole) {
             // The CTA that brings a segment's last part joins all of them, in their order. The arrival count of a
             // segment is back at 0 after.
-            const int first = pl.u0 + u - off;
+            const int first = before + seg * (units + kSegment) + kSegment;
             const int c0 = pl.c0 >= 0 ? pl.c0 : pl.owner(first), c1 = pl.c0 >= 0 ? pl.c1 : pl.owner(first + units - 1);
             if (threadIdx.x == 0) {
                 // The 4-bit fields of CTAs c0 .. c1 - 1 are this segment's alone: one counts up to 15 parts, and
