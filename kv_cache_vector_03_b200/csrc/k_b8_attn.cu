@@ -316,6 +316,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     }
     const int mine = pl.mine;
     if (mine <= 0) return;
+    // (what is not needed before a segment's end waits in shared memory)
+    __shared__ Plan s_plan;
+    __shared__ int s_before;
+    if (threadIdx.x == 0) {
+        s_plan = pl;
+        s_before = pl.before;
+    }
 
     // Unit i of the share goes to warp i mod NW and stage i mod ST; who has consumed a stage refills it with
     // unit i + ST. The k-th unit that this warp issues is a(k) = w + NW k for the first `early` ones, which it
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         ++issued;
     };
 
-    int i = w, v = pl.virt, x0 = pl.x, before = pl.before;   // i: this warp's next unit, in stage st
+    int i = w, v = pl.virt, x0 = pl.x;               // i: this warp's next unit, in stage st
     int st = w % ST;
     uint32_t phase = 0;
     // where a lane's values (tokens 2 tq, 2 tq + 1) lie in a page; 8 tokens on is 8 D on
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll 1
         while (x0 >= (units = virt_units<SP>(p, v, n)) * segs && v + 1 < n_virt) {
             x0 -= units * segs;
-            before += units ? (units + kSegment) * segs : 0;
+            if (threadIdx.x == 0 && units) s_before += (units + kSegment) * segs;
             ++v;
         }
         const int seg = x0 / units, off = x0 - seg * units;
@@ -900,8 +907,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         if (!whole) {
             // The CTA that brings a segment's last part joins all of them, in their order. The arrival count of a
             // segment is back at 0 after.
-            const int first = before + seg * (units + kSegment) + kSegment;
-            const int c0 = pl.c0 >= 0 ? pl.c0 : pl.owner(first), c1 = pl.c0 >= 0 ? pl.c1 : pl.owner(first + units - 1);
+            const int first = s_before + seg * (units + kSegment) + kSegment;
+            const int c0 = s_plan.c0 >= 0 ? s_plan.c0 : s_plan.owner(first);
+            const int c1 = s_plan.c0 >= 0 ? s_plan.c1 : s_plan.owner(first + units - 1);
             if (threadIdx.x == 0) {
                 // The 4-bit fields of CTAs c0 .. c1 - 1 are this segment's alone: one counts up to 15 parts, and
                 // in 15 fields or more there is a whole 16-bit one.
