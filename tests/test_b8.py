@@ -134,6 +134,7 @@ def test_attention_refusals(lib):
                     wb=need - 1) == lib.TQ_ERR_WORKSPACE
     assert lib.lib.tq_b8_workspace_bytes(ctypes.byref(host_cache(lib, d=12)), 1, 4, 0, 0) == 0
     assert lib.lib.tq_b8_workspace_bytes(r, 128, 129, 0, 0) == 0
+    assert lib.lib.tq_b8_workspace_bytes(r, 0, 0, 0, 0) >= 256
 
 
 def test_select_and_evict_refusals(lib):
