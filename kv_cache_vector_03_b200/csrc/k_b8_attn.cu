@@ -981,41 +981,58 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     }
 }
 
-// acc_out[t] = decay * acc_in[t] + sum over rows of 2^(logit - lse), rows in order: one thread per
-// token, so nothing is added atomically. With a selection a table in shared memory says which of
-// its entries holds a block.
-__global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int64_t tiles) {
+// acc_out[t] = decay * acc_in[t] + sum over rows of 2^(logit - lse), rows in order: one thread adds up a token, so
+// nothing is added atomically. A thread has kAccPer tokens and takes four rows at a time, to have that many loads under
+// way. With a selection a table in shared memory says which of its entries holds a block.
+constexpr int kAccPer = 2, kAccTile = kAccTok * kAccPer;
+__global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int tiles) {
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
-    const int64_t sh = blockIdx.x / tiles, s = sh / c.n_kv;
-    const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g;
-    const int64_t t0 = (blockIdx.x - sh * tiles) * kAccTok, t = t0 + threadIdx.x;
+    const int sh = blockIdx.x / tiles, s = sh / c.n_kv;
+    const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g, t0 = (blockIdx.x - sh * tiles) * kAccTile;
     if (t0 >= n) return;
-    __shared__ int s_at[kAccTok / 32];
+    __shared__ int s_at[kAccTile / 32];
     if (p.sel) {
-        if (threadIdx.x < kAccTok / 32) s_at[threadIdx.x] = t0 / 32 + threadIdx.x == nfull ? p.n_sel : -1;
+        if (threadIdx.x < kAccTile / 32) s_at[threadIdx.x] = t0 / 32 + threadIdx.x == nfull ? p.n_sel : -1;
         __syncthreads();
         for (int u = threadIdx.x; u < p.n_sel; u += kAccTok) {
-            const int b = p.sel[sh * p.n_sel + u] - (int)(t0 / 32);
-            if (b >= 0 && b < kAccTok / 32 && b + t0 / 32 < nfull) s_at[b] = u;
+            const int b = p.sel[(int64_t)sh * p.n_sel + u] - t0 / 32;
+            if (b >= 0 && b < kAccTile / 32 && b + t0 / 32 < nfull) s_at[b] = u;
         }
         __syncthreads();
     }
-    if (t >= n) return;
-    const int64_t at = sh * c.max_blocks * 32 + t;
-    float a = p.acc_in && t < n - p.n_q ? p.decay * p.acc_in[at] : 0.f;
-    const int u = p.sel ? s_at[threadIdx.x >> 5] : (int)(t >> 5);
-    if (u >= 0) {
-        const float* lg = p.logits + sh * rows * p.logit_row + (int64_t)u * 32 + (t & 31);
-        float w = 0.f;
-        for (int r = 0; r < rows; ++r) {
-            const float e = p.lse[sh * rows + r];
-            if (e != INFINITY) w += tq_exp2(lg[r * p.logit_row] - e);
-        }
-        a += w;
+    const float* lse = p.lse + (int64_t)sh * rows;
+    float a[kAccPer], w[kAccPer];
+    const float* lg[kAccPer];
+    const int64_t at = (int64_t)sh * c.max_blocks * 32;
+#pragma unroll
+    for (int k = 0; k < kAccPer; ++k) {
+        const int i = threadIdx.x + k * kAccTok, t = t0 + i;
+        a[k] = p.acc_in && t < n - p.n_q ? p.decay * p.acc_in[at + t] : 0.f;
+        const int u = t >= n ? -1 : p.sel ? s_at[i >> 5] : t >> 5;
+        lg[k] = u < 0 ? nullptr : p.logits + (int64_t)sh * rows * p.logit_row + (int64_t)u * 32 + (t & 31);
+        w[k] = 0.f;
     }
-    p.acc_out[at] = a;
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+        float e[4], y[kAccPer][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            e[r] = r0 + r < rows ? lse[r0 + r] : INFINITY;
+#pragma unroll
+            for (int k = 0; k < kAccPer; ++k) y[k][r] = lg[k] && r0 + r < rows ? lg[k][(r0 + r) * p.logit_row] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int k = 0; k < kAccPer; ++k)
+                if (lg[k] && e[r] != INFINITY) w[k] += tq_exp2(y[k][r] - e[r]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAccPer; ++k) {
+        const int t = t0 + threadIdx.x + k * kAccTok;
+        if (t < n) p.acc_out[at + t] = a[k] + w[k];
+    }
 }
 
 template <int D, int NT, bool WT, bool SP>
@@ -1039,7 +1056,7 @@ int b8_attn_grid() { return std::min(kCtasPerSm * tq_device_sms(), 2 * kB8Counte
 
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     const int64_t virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
-    const int64_t tiles = (p.c.max_blocks * 32 + kAccTok - 1) / kAccTok;
+    const int64_t tiles = (p.c.max_blocks * 32 + kAccTile - 1) / kAccTile;
     // the kernel counts units in 31 bits
     const int64_t most = (p.sel ? p.n_sel : p.c.max_blocks) + 1;
     if (virt * p.c.n_kv * p.row_tiles > 0x3fffffffLL || most * (virt * p.c.n_kv * p.row_tiles) > 0x3fffffffLL)
@@ -1051,5 +1068,5 @@ cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     else if (p.c.D == 128) e = wide ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
     else e = launch<256, 1>(p, st);
     if (e != cudaSuccess || !p.acc_out) return e;
-    return tq_launch_pdl(k_b8_acc, dim3((unsigned)(tiles * p.c.n_seq * p.c.n_kv)), dim3(kAccTok), 0, st, p, tiles);
+    return tq_launch_pdl(k_b8_acc, dim3((unsigned)(tiles * p.c.n_seq * p.c.n_kv)), dim3(kAccTok), 0, st, p, (int)tiles);
 }

@@ -10,6 +10,7 @@
 // found digit by digit (11 + 11 + 10 bits) from histograms in shared memory; a last pass in
 // index order writes what lies above it and the first of what equals it, by prefix sums, so the
 // result is ascending and ties go to the lowest index.
+#include <algorithm>
 #include <cfloat>
 
 #include "k_b8.cuh"
@@ -31,47 +32,46 @@ TQ_DEVICE int candidates(int n, int n_q, int i) {
     return last < 0 ? 0 : min(n >> 5, (last >> 5) + 1);
 }
 
+// One CTA per row (sequence, query token, kv head) and range of blocks: its warps take 16 blocks each in turn; the first
+// summaries are on their way while the query heads become int8.
 template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int tiles) {
+__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int ranges, int range) {
     constexpr int CH = D / 32;       // 16-byte chunks a lane takes of a summary's 2 D bytes
+    constexpr int STEP = kScoreWarps * 16;
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    int64_t rowid = blockIdx.x / tiles;
-    const int tile = (int)(blockIdx.x - rowid * tiles);
-    const int64_t out0 = rowid * c.max_blocks;
-    const int h = (int)(rowid % c.n_kv);
-    rowid /= c.n_kv;
-    const int i = (int)(rowid % p.n_q);
-    const int64_t s = rowid / p.n_q;
-    const int nb = candidates(b8_len(c, s), p.n_q, i);
-    const int b0 = (tile * kScoreWarps + w) * 16;
-    if (tile * kScoreWarps * 16 >= nb) return;
+    const int row = blockIdx.x / ranges, si = row / c.n_kv, h = row - si * c.n_kv, s = p.n_q == 1 ? si : si / p.n_q;
+    const int from = (blockIdx.x - row * ranges) * range;
+    const int nb = min(candidates(b8_len(c, s), p.n_q, si - s * p.n_q), from + range);
+    if (from >= nb) return;
     __shared__ uint32_t s_q[8][2 * D / 4 + 4];   // + 4 words: the 8 rows of a load fall on distinct banks
     __shared__ float s_step[8];
-    // the summaries of this warp's 16 blocks: rows gq and gq + 8
-    uint4 a[2][CH];
+    const int32_t* table = c.table + s * c.max_blocks;
+    uint32_t* key = p.key + row * c.max_blocks;
+    uint4 a[2][CH];                  // summaries and key scales of rows gq and gq + 8 of 16 blocks
     float ks[2];
+    auto load = [&](int b0) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int b = b0 + gq + 8 * r;
-        const uint8_t* e = nullptr;
-        if (b < nb) {
-            uint8_t* page = b8_page(c, c.table[s * c.max_blocks + b]);
-            if (page) e = b8_entry(c, page, h);
+        for (int r = 0; r < 2; ++r) {
+            const uint8_t* e = nullptr;
+            if (b0 + gq + 8 * r < nb) {
+                uint8_t* page = b8_page(c, table[b0 + gq + 8 * r]);
+                if (page) e = b8_entry(c, page, h);
+            }
+            ks[r] = e ? *reinterpret_cast<const float*>(e) : 0.f;
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+                a[r][k] = e ? *reinterpret_cast<const uint4*>(e + 32 + 16 * (tq + 4 * k)) : make_uint4(0u, 0u, 0u, 0u);
         }
-        ks[r] = e ? *reinterpret_cast<const float*>(e) : 0.f;
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-            a[r][k] = e ? *reinterpret_cast<const uint4*>(e + 32 + 16 * (tq + 4 * k)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    float best[2] = {-INFINITY, -INFINITY};
-    for (int g0 = 0; g0 < p.g; g0 += 8) {
+    };
+    for (int g0 = 0; g0 < p.g; g0 += 8) {        // 8 query heads at a time
+        load(from + 16 * w);
         if (g0) __syncthreads();
         {   // warp w holds query head g0 + w as int8: negative parts against lo, positive ones against hi
             const int j = g0 + w;
-            const int64_t at = (((s * p.n_q + i) * c.n_kv + h) * p.g + j) * c.d;
+            const int64_t at = ((int64_t)row * p.g + j) * c.d;
             float v[D / 32], am = 0.f;
             bool fin = true;
 #pragma unroll
@@ -94,26 +94,33 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
             if (lane == 0) s_step[w] = live ? am * kB8Inv127 : 0.f;
         }
         __syncthreads();
-        int acc[4] = {0, 0, 0, 0};
+        for (int b0 = from + 16 * w; b0 < nb; b0 += STEP) {
+            if (b0 != from + 16 * w) load(b0);
+            int acc[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < CH; ++k) {
-            const uint32_t* b = &s_q[gq][4 * (tq + 4 * k)];
-            tq_imma(acc, a[0][k].x, a[1][k].x, a[0][k].y, a[1][k].y, b[0], b[1]);
-            tq_imma(acc, a[0][k].z, a[1][k].z, a[0][k].w, a[1][k].w, b[2], b[3]);
+            for (int k = 0; k < CH; ++k) {
+                const uint32_t* b = &s_q[gq][4 * (tq + 4 * k)];
+                tq_imma(acc, a[0][k].x, a[1][k].x, a[0][k].y, a[1][k].y, b[0], b[1]);
+                tq_imma(acc, a[0][k].z, a[1][k].z, a[0][k].w, a[1][k].w, b[2], b[3]);
+            }
+            float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {        // blocks gq, gq, gq + 8, gq + 8; heads 2 tq, 2 tq + 1
+                const int j = 2 * tq + (k & 1);
+                if (g0 + j < p.g)
+                    best[k >> 1] = fmaxf(best[k >> 1], __fmul_rn(__fmul_rn((float)acc[k], ks[k >> 1]), s_step[j]));
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+                best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+                const int b = b0 + gq + 8 * r;
+                if (tq == 0 && b < nb) {         // (a block's key is this lane's alone, in every round of heads)
+                    const uint32_t u = order_bits(best[r]);
+                    key[b] = g0 ? max(key[b], u) : u;
+                }
+            }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {   // blocks gq, gq, gq + 8, gq + 8; heads 2 tq, 2 tq + 1
-            const int j = 2 * tq + (k & 1);
-            if (g0 + j < p.g)
-                best[k >> 1] = fmaxf(best[k >> 1], __fmul_rn(__fmul_rn((float)acc[k], ks[k >> 1]), s_step[j]));
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-        const int b = b0 + gq + 8 * r;
-        if (tq == 0 && b < nb) p.key[out0 + b] = order_bits(best[r]);
     }
 }
 
@@ -414,18 +421,20 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
 
 cudaError_t b8_launch_select(const B8SelectParams& p, cudaStream_t st) {
     const int64_t rows = p.c.n_seq * p.n_q * p.c.n_kv;
-    const int64_t tiles = (p.c.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
-    if (rows * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(rows * tiles)), block(kScoreWarps * 32);
+    // Ranges of blocks: a step of 128 each, longer where that gives more than four waves of CTAs
+    const int64_t steps = (p.c.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16), slots = 16 * (int64_t)tq_device_sms();
+    const int64_t per = std::max<int64_t>(1, (rows * steps + slots - 1) / slots), ranges = (steps + per - 1) / per;
+    if (rows * ranges > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(rows * ranges)), block(kScoreWarps * 32);
     const cudaError_t e = tq_launch_pdl(p.c.D == 64    ? k_b8_score<64>
                                         : p.c.D == 128 ? k_b8_score<128>
                                                        : k_b8_score<256>,
-                                        grid, block, 0, st, p, (int)tiles);
+                                        grid, block, 0, st, p, (int)ranges, (int)(per * kScoreWarps * 16));
     if (e != cudaSuccess) return e;
-    // the fewest threads whose registers hold a whole row: many rows fit an SM, and little code runs
+    // as few keys a thread as hold a whole row: little code runs
     const dim3 r((unsigned)rows);
     if (p.c.max_blocks <= 1024) return tq_launch_pdl(k_b8_pick_blocks<256, 4>, r, dim3(256), 0, st, p);
-    if (p.c.max_blocks <= 4096) return tq_launch_pdl(k_b8_pick_blocks<512, 8>, r, dim3(512), 0, st, p);
+    if (p.c.max_blocks <= 4096) return tq_launch_pdl(k_b8_pick_blocks<1024, 4>, r, dim3(1024), 0, st, p);
     return tq_launch_pdl(k_b8_pick_blocks<1024, 16>, r, dim3(1024), 0, st, p);
 }
 
@@ -436,7 +445,8 @@ cudaError_t b8_launch_evict(const B8EvictParams& p, cudaStream_t st) {
     const dim3 r((unsigned)rows);
     const int64_t most = p.c.max_blocks * 32;
     const cudaError_t e = most <= 1024   ? tq_launch_pdl(k_b8_pick_tokens<256, 4>, r, dim3(256), 0, st, p)
-                          : most <= 4096 ? tq_launch_pdl(k_b8_pick_tokens<512, 8>, r, dim3(512), 0, st, p)
+                          : most <= 4096 ? tq_launch_pdl(k_b8_pick_tokens<1024, 4>, r, dim3(1024), 0, st, p)
+                          : most <= 8192 ? tq_launch_pdl(k_b8_pick_tokens<1024, 8>, r, dim3(1024), 0, st, p)
                                          : tq_launch_pdl(k_b8_pick_tokens<1024, 16>, r, dim3(1024), 0, st, p);
     if (e != cudaSuccess) return e;
     return tq_launch_pdl(p.c.D == 64 ? k_b8_move<64> : p.c.D == 128 ? k_b8_move<128> : k_b8_move<256>,
