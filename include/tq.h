@@ -301,7 +301,7 @@ int tq_q8_logits(const void* packed, int d, int64_t n_seq, int n_kv, int64_t n_t
  *   n_kv       kv heads, 1..1024.
  *   n_seq      sequences, 0..65535.
  *   n_pages    pages in the pool, < 2^31.
- *   max_blocks entries of a table row, 1..2^25: a sequence holds at most 32 max_blocks tokens.
+ *   max_blocks entries of a table row, 1..2^23: a sequence holds at most 32 max_blocks tokens.
  *   pages      device, n_pages * tq_b8_page_bytes(d, n_kv) bytes, 128-byte aligned.
  *   table      device int32 [n_seq, max_blocks], page numbers. Only the entries of full blocks are
  *              read (and, by append, of the blocks it fills). Two sequences may share pages that
@@ -343,8 +343,10 @@ size_t tq_b8_page_bytes(int d, int n_kv);
 
 /* Workspace of any tq_b8 call on this cache, 256-byte aligned, status word first. n_q, g: as in
  * tq_b8_attention and tq_b8_select (0 if neither is called); n_sel: entries of a selection (0:
- * none); weights: nonzero if tq_b8_attention is called with acc_out. 0 if unsupported. Calls
- * whose work may overlap (other streams, graphs) need workspaces of their own.            */
+ * none); weights: nonzero if tq_b8_attention is called with acc_out. 0 if unsupported. A call with a
+ * selection and one without need the larger of the two sizes. The first 256 bytes must be zero before the first
+ * call (tq_reset_status); calls leave their part of them so. Calls whose work may overlap (other streams,
+ * graphs) need workspaces of their own.                                                   */
 size_t tq_b8_workspace_bytes(const tq_b8_cache* cache, int n_q, int g, int n_sel, int weights);
 
 /* Appends tokens. len already counts them: token j of sequence s takes position
@@ -369,7 +371,9 @@ int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dty
  *   out = sum_t w_t v_t,  w = softmax over t <= p of scale <q, k_t>.
  * A query whose position is negative, or that sees no token, gives zeros.
  *   q         device [n_seq, n_q, n_kv * g, d], fp32 or bf16, 16-byte aligned; n_q, g >= 1,
- *             n_q * g <= 16384.
+ *             n_q * g <= 16384. Blocks times query rows are limited too: with n_q * g (with sel, g) rows in
+ *             tiles of 8 (16 above 8 rows, for d <= 128), sequences (with sel, times n_q) x kv heads x tiles x
+ *             (max_blocks + 1, or n_sel + 1) up to 2^30, else TQ_ERR_UNSUPPORTED.
  *   sel       device int32 [n_seq, n_q, n_kv, n_sel] block numbers from tq_b8_select: the query
  *             sees only tokens of these blocks and of the open block; entries outside the
  *             full blocks are passed over; an entry that is named twice counts twice. NULL with
@@ -430,8 +434,8 @@ int tq_dequantize(const tq_codec* codec, const void* packed, int64_t n_streams, 
                   float* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Status word. Data-dependent faults of every call that used `ws` accumulate in its first
- * word until read. tq_reset_status enqueues a clear (do it once on a new workspace);
- * tq_get_status synchronises `stream`, reads the word and clears it, returning TQ_OK,
+ * word until read. tq_reset_status enqueues a clear of those 256 bytes (do it once on a new
+ * workspace); tq_get_status synchronises `stream`, reads the word and clears it, returning TQ_OK,
  * TQ_ERR_TIMEOUT if a bounded wait of a kernel ran out (it takes precedence), TQ_ERR_RANGE,
  * or TQ_ERR_CUDA if the read itself failed.                                              */
 int tq_reset_status(void* ws, void* stream);

@@ -985,53 +985,55 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 // nothing is added atomically. A thread has kAccPer tokens and takes four rows at a time, to have that many loads under
 // way. With a selection a table in shared memory says which of its entries holds a block.
 constexpr int kAccPer = 2, kAccTile = kAccTok * kAccPer;
-__global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int tiles) {
+__global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int splits) {
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
-    const int sh = blockIdx.x / tiles, s = sh / c.n_kv;
-    const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g, t0 = (blockIdx.x - sh * tiles) * kAccTile;
-    if (t0 >= n) return;
-    __shared__ int s_at[kAccTile / 32];
-    if (p.sel) {
-        if (threadIdx.x < kAccTile / 32) s_at[threadIdx.x] = t0 / 32 + threadIdx.x == nfull ? p.n_sel : -1;
-        __syncthreads();
-        for (int u = threadIdx.x; u < p.n_sel; u += kAccTok) {
-            const int b = p.sel[(int64_t)sh * p.n_sel + u] - t0 / 32;
-            if (b >= 0 && b < kAccTile / 32 && b + t0 / 32 < nfull) s_at[b] = u;
-        }
-        __syncthreads();
-    }
+    const int sh = blockIdx.x / splits, s = sh / c.n_kv;
+    const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g;
     const float* lse = p.lse + (int64_t)sh * rows;
-    float a[kAccPer], w[kAccPer];
-    const float* lg[kAccPer];
     const int64_t at = (int64_t)sh * c.max_blocks * 32;
+    __shared__ int s_at[kAccTile / 32];
+    for (int t0 = (blockIdx.x - sh * splits) * kAccTile; t0 < n; t0 += splits * kAccTile) {
+        if (p.sel) {
+            __syncthreads();
+            if (threadIdx.x < kAccTile / 32) s_at[threadIdx.x] = t0 / 32 + threadIdx.x == nfull ? p.n_sel : -1;
+            __syncthreads();
+            for (int u = threadIdx.x; u < p.n_sel; u += kAccTok) {
+                const int b = p.sel[(int64_t)sh * p.n_sel + u] - t0 / 32;
+                if (b >= 0 && b < kAccTile / 32 && b + t0 / 32 < nfull) s_at[b] = u;
+            }
+            __syncthreads();
+        }
+        float a[kAccPer], w[kAccPer];
+        const float* lg[kAccPer];
 #pragma unroll
-    for (int k = 0; k < kAccPer; ++k) {
-        const int i = threadIdx.x + k * kAccTok, t = t0 + i;
-        a[k] = p.acc_in && t < n - p.n_q ? p.decay * p.acc_in[at + t] : 0.f;
-        const int u = t >= n ? -1 : p.sel ? s_at[i >> 5] : t >> 5;
-        lg[k] = u < 0 ? nullptr : p.logits + (int64_t)sh * rows * p.logit_row + (int64_t)u * 32 + (t & 31);
-        w[k] = 0.f;
-    }
-    for (int r0 = 0; r0 < rows; r0 += 4) {
-        float e[4], y[kAccPer][4];
+        for (int k = 0; k < kAccPer; ++k) {
+            const int i = threadIdx.x + k * kAccTok, t = t0 + i;
+            a[k] = p.acc_in && t < n - p.n_q ? p.decay * p.acc_in[at + t] : 0.f;
+            const int u = t >= n ? -1 : p.sel ? s_at[i >> 5] : t >> 5;
+            lg[k] = u < 0 ? nullptr : p.logits + (int64_t)sh * rows * p.logit_row + (int64_t)u * 32 + (t & 31);
+            w[k] = 0.f;
+        }
+        for (int r0 = 0; r0 < rows; r0 += 4) {
+            float e[4], y[kAccPer][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            e[r] = r0 + r < rows ? lse[r0 + r] : INFINITY;
+            for (int r = 0; r < 4; ++r) {
+                e[r] = r0 + r < rows ? lse[r0 + r] : INFINITY;
 #pragma unroll
-            for (int k = 0; k < kAccPer; ++k) y[k][r] = lg[k] && r0 + r < rows ? lg[k][(r0 + r) * p.logit_row] : 0.f;
+                for (int k = 0; k < kAccPer; ++k) y[k][r] = lg[k] && r0 + r < rows ? lg[k][(r0 + r) * p.logit_row] : 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < kAccPer; ++k)
+                    if (lg[k] && e[r] != INFINITY) w[k] += tq_exp2(y[k][r] - e[r]);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int k = 0; k < kAccPer; ++k)
-                if (lg[k] && e[r] != INFINITY) w[k] += tq_exp2(y[k][r] - e[r]);
-    }
-#pragma unroll
-    for (int k = 0; k < kAccPer; ++k) {
-        const int t = t0 + threadIdx.x + k * kAccTok;
-        if (t < n) p.acc_out[at + t] = a[k] + w[k];
+        for (int k = 0; k < kAccPer; ++k) {
+            const int t = t0 + threadIdx.x + k * kAccTok;
+            if (t < n) p.acc_out[at + t] = a[k] + w[k];
+        }
     }
 }
 
@@ -1056,17 +1058,18 @@ int b8_attn_grid() { return std::min(kCtasPerSm * tq_device_sms(), 2 * kB8Counte
 
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     const int64_t virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
-    const int64_t tiles = (p.c.max_blocks * 32 + kAccTile - 1) / kAccTile;
     // the kernel counts units in 31 bits
     const int64_t most = (p.sel ? p.n_sel : p.c.max_blocks) + 1;
     if (virt * p.c.n_kv * p.row_tiles > 0x3fffffffLL || most * (virt * p.c.n_kv * p.row_tiles) > 0x3fffffffLL)
         return cudaErrorInvalidValue;
-    if (p.acc_out && tiles * p.c.n_seq * p.c.n_kv > 0x7fffffffLL) return cudaErrorInvalidValue;
     const bool wide = p.row_tile == 16;
     cudaError_t e;
     if (p.c.D == 64) e = wide ? launch<64, 2>(p, st) : launch<64, 1>(p, st);
     else if (p.c.D == 128) e = wide ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
     else e = launch<256, 1>(p, st);
     if (e != cudaSuccess || !p.acc_out) return e;
-    return tq_launch_pdl(k_b8_acc, dim3((unsigned)(tiles * p.c.n_seq * p.c.n_kv)), dim3(kAccTok), 0, st, p, (int)tiles);
+    // one CTA per tile of tokens; fewer, which go on, where the capacity gives many more than 32 an SM
+    const int64_t rows = p.c.n_seq * p.c.n_kv, tiles = (p.c.max_blocks * 32 + kAccTile - 1) / kAccTile;
+    const int64_t splits = std::max<int64_t>(1, std::min(tiles, 32 * (int64_t)tq_device_sms() / rows));
+    return tq_launch_pdl(k_b8_acc, dim3((unsigned)(rows * splits)), dim3(kAccTok), 0, st, p, (int)splits);
 }

@@ -12,7 +12,7 @@
 namespace {
 
 static_assert(64 + kB8Counters <= TQ_STATUS_BYTES, "the arrival counts share the status word's bytes");
-constexpr int64_t kMaxBlocks = (int64_t)1 << 25;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
 
 size_t align_up(size_t v) { return (v + TQ_ALIGN - 1) / TQ_ALIGN * TQ_ALIGN; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

@@ -65,7 +65,7 @@ def host_cache(lib, d=128, n_kv=8, n_seq=2, n_pages=64, max_blocks=16, pages=0x1
 
 
 BAD_CACHES = [dict(d=12), dict(d=264), dict(d=0), dict(n_kv=0), dict(n_kv=1025), dict(n_seq=-1), dict(n_seq=65536),
-              dict(n_pages=-1), dict(n_pages=1 << 31), dict(max_blocks=0), dict(max_blocks=(1 << 25) + 1),
+              dict(n_pages=-1), dict(n_pages=1 << 31), dict(max_blocks=0), dict(max_blocks=(1 << 23) + 1),
               dict(pages=None), dict(pages=0x10040), dict(table=None), dict(table=0x20002), dict(length=None),
               dict(open_=None), dict(open_=0x40008)]
 
@@ -733,3 +733,160 @@ def test_pool_beyond_4_gib(m):
     assert p.ok(ws) and p.ok()
     want, _, size, reach = ref.attention(p.seqs[0], q64[0], 0.1)
     close(out[0].double().cpu().numpy().reshape(want.shape), want, size, reach, d)
+
+
+@pytest.mark.gpu
+def test_values_that_a_query_does_not_see(m):
+    """Several new tokens, the last of which are not finite in keys and values: queries before them answer as
+    if they were not there, those that see them do not."""
+    import torch
+    for d, n_old in ((64, 37), (128, 64), (200, 13)):
+        p = Pair(m, d, 2, 1, 4, 98)
+        p.append([n_old])
+        k, v = p.tokens(3)
+        kb, vb = k.copy(), v.copy()
+        kb[1, 0, 3], vb[1, 0, 5], vb[2, 1, 0], kb[2, 1, 1] = np.nan, np.inf, np.nan, -np.inf
+        p.length += 3
+        p.seqs[0].append(k, v)
+        m.tq_b8_append(p.cache, torch.from_numpy(kb[None]).cuda(), torch.from_numpy(vb[None]).cuda(), p.ws)
+        q, q64 = p.queries(3, 2, "bf16")
+        ws = p.workspace(3, 2)
+        out = torch.zeros(q.shape, device="cuda")
+        m.tq_b8_attention(p.cache, q, 0.1, out, ws)
+        assert p.ok(ws)
+        got = out.double().cpu().numpy().reshape(q64.shape)[0]
+        want, _, size, reach = ref.attention(p.seqs[0], q64[0], 0.1)
+        close(got[0], want[0], size[0], reach[0], d)
+        close(got[1, 1], want[1, 1], size[1, 1], reach[1, 1], d)      # head 1 is hurt by the last token only
+        assert not np.isfinite(got[1, 0]).all() and not np.isfinite(got[2]).all()
+
+
+@pytest.mark.gpu
+def test_read_and_evict_bad_pages(m):
+    """A source page outside the pool counts as zeros and is left out of reads; a target page outside it is
+    not written; both are reported."""
+    import torch
+    p = Pair(m, 64, 1, 1, 6, 99, spare=6)
+    p.append([192])
+    table = p.table.clone()
+    table[0, 2] = p.pages.shape[0]
+    c = m.Cache8(64, p.pages, table, p.length, p.open_)
+    k, v = (torch.full((1, 192, 1, 64), 768.0, device="cuda") for _ in range(2))
+    m.tq_b8_read(c, k, v, p.ws)
+    assert m.tq_get_status(p.ws) == m.TQ_ERR_RANGE
+    x = p.seqs[0].values()
+    for side, got in enumerate((k, v)):
+        g = got[0, :, 0].double().cpu().numpy()
+        assert (g[64:96] == 768.0).all()
+        keep = np.r_[0:64, 96:192]
+        assert np.all(np.abs(g[keep] - x[keep, 0, side]) <= 2.0 ** -24 * np.abs(x[keep, 0, side]) + 1e-40)
+    acc = torch.arange(192, dtype=torch.float32, device="cuda").reshape(1, 1, 192)
+    dst = torch.from_numpy(p.names[6:].reshape(1, 6).copy()).cuda()
+    dst[0, 1] = -7
+    kept, length = torch.zeros(1, 1, 96, dtype=torch.int32, device="cuda"), torch.zeros_like(p.length)
+    acc_out, before = torch.zeros_like(acc), p.pages.clone()
+    m.tq_b8_evict(c, acc, 3, dst, kept, length, acc_out, p.ws, n_first=64)
+    assert m.tq_get_status(p.ws) == m.TQ_ERR_RANGE
+    assert kept[0, 0].tolist() == list(range(64)) + list(range(160, 192)) and length.tolist() == [96]
+    assert acc_out[0, 0, :96].tolist() == [float(t) for t in kept[0, 0].tolist()]
+    written = (p.pages != before).any(dim=1).nonzero().flatten().tolist()
+    assert set(written) <= {int(dst[0, 0]), int(dst[0, 2])}
+
+
+@pytest.mark.gpu
+def test_evict_and_select_of_long_rows(m):
+    """Rows longer than the choosing kernel keeps in registers: 20011 tokens, 17000 blocks."""
+    import torch
+    p = Pair(m, 8, 1, 1, 626, 101, spare=626)
+    p.append([20011])
+    acc = torch.rand(1, 1, 626 * 32, device="cuda")
+    acc[0, 0, 5000:9000] = 0.5                                        # a tie across the border
+    dst = torch.from_numpy(p.names[626:].reshape(1, 626).copy()).cuda()
+    for keep in (10, 313, 600):
+        kept, length = torch.zeros(1, 1, 32 * keep, dtype=torch.int32, device="cuda"), torch.zeros_like(p.length)
+        m.tq_b8_evict(p.cache, acc, keep, dst, kept, length, torch.zeros_like(acc), p.ws, n_first=5, n_last=100)
+        want = ref.choose(acc[0, 0].cpu().numpy(), 625 * 32, 32 * keep, 5, 100)
+        assert np.array_equal(kept[0, 0].cpu().numpy(), want)
+    # block selection: only lengths, tables and summaries matter
+    nb = 17000
+    d, n_pages = 8, 64
+    pages = torch.zeros(n_pages, m.tq_b8_page_bytes(d, 1), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(3)
+    lo = rng.integers(-127, 1, (n_pages, d)).astype(np.int8)
+    hi = rng.integers(0, 128, (n_pages, d)).astype(np.int8)
+    scale = rng.uniform(0.01, 0.02, n_pages).astype(np.float32)
+    host = np.zeros((n_pages, 32 + 128), np.uint8)
+    host[:, :4] = scale.view(np.uint8).reshape(-1, 4)
+    host[:, 32:32 + d], host[:, 96:96 + d] = lo.view(np.uint8), hi.view(np.uint8)
+    pages[:, :160] = torch.from_numpy(host).cuda()
+    table = torch.from_numpy(rng.integers(0, n_pages, (1, nb)).astype(np.int32)).cuda()      # pages many times over: ties
+    length = torch.full((1,), nb * 32, dtype=torch.int32, device="cuda")
+    c = m.Cache8(d, pages, table, length, torch.zeros(1, 1, 2, 32, d, dtype=torch.bfloat16, device="cuda"))
+    q = torch.randn(1, 1, 2, d, device="cuda")
+    for n_sel in (3, 500, 16500):
+        ws = m.workspace(m.tq_b8_workspace_bytes(c, 1, 2, n_sel))
+        sel = torch.zeros(1, 1, 1, n_sel, dtype=torch.int32, device="cuda")
+        m.tq_b8_select(c, q, sel, ws)
+        assert m.tq_get_status(ws) == m.TQ_OK
+        best = np.full(n_pages, -np.inf, np.float32)
+        for x in q[0, 0].double().cpu().numpy():
+            a = np.float32(np.abs(x).max())
+            qi = np.rint(x * np.float64(np.float32(1) / a * np.float32(127)))
+            whole = np.maximum(qi * lo, qi * hi).sum(axis=1).astype(np.float32)
+            best = np.maximum(best, whole * scale * (a * ref.INV127))
+        want = ref.choose(best[table[0].cpu().numpy()], nb, n_sel, 1, 1)
+        assert np.array_equal(sel[0, 0, 0].cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+def test_streams_graphs_and_workspaces(m):
+    """Calls at once on two streams with workspaces of their own; two captured graphs that share one
+    workspace, replayed in turn; a workspace that other calls have used; a reset workspace."""
+    import torch
+    d, n_kv, g = 128, 4, 4
+    p = Pair(m, d, n_kv, 3, 70, 102)
+    p.append([2200, 700, 33])
+    qs, outs, want = [], [], []
+    for _ in range(2):
+        q, q64 = p.queries(1, g, "bf16")
+        qs.append(q)
+        outs.append(torch.zeros(q.shape, device="cuda"))
+        want.append([ref.attention(sq, q64[s], 0.1) for s, sq in enumerate(p.seqs)])
+
+    def check():
+        for out, w in zip(outs, want):
+            got = out.double().cpu().numpy().reshape(3, 1, n_kv, g, d)
+            for s in range(3):
+                close(got[s], w[s][0], w[s][2], w[s][3], d)
+            out.zero_()
+
+    need = m.tq_b8_workspace_bytes(p.cache, 1, g)
+    dirty = torch.randint(1, 255, (need,), dtype=torch.uint8, device="cuda")
+    m.tq_reset_status(dirty)
+    assert (dirty[:256] == 0).all() and (dirty[256:] != 0).any()
+    spaces = [dirty, m.workspace(need)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for q, out, ws, st in zip(qs, outs, spaces, streams):
+            m.tq_b8_attention(p.cache, q, 0.1, out, ws, stream=st)
+    torch.cuda.synchronize()
+    check()
+    graphs = []
+    for q, out in zip(qs, outs):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            m.tq_b8_attention(p.cache, q, 0.1, out, dirty)
+        graphs.append(gr)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    check()
+    x = torch.randn(2, 64, d, device="cuda")
+    packed = torch.zeros(m.tq_q8_packed_bytes(d, 2, 64), dtype=torch.uint8, device="cuda")
+    for q, out in zip(qs, outs):
+        m.tq_q8_quantize(x, d, 2, 64, 64 * d, packed, dirty)
+        m.tq_b8_attention(p.cache, q, 0.1, out, dirty)
+    check()
+    assert m.tq_get_status(dirty) == m.TQ_OK and (dirty[:256] == 0).all()
