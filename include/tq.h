@@ -352,7 +352,7 @@ size_t tq_b8_workspace_bytes(const tq_b8_cache* cache, int n_q, int g, int n_sel
 /* Appends tokens. len already counts them: token j of sequence s takes position
  * len[s] - add[s] + j.
  *   k, v      device, fp32 or bf16, 16-byte aligned: element (s, j, h, i) at s * seq_stride +
- *             j * tok_stride + h * d + i, j < n_new; strides in elements, multiples of 8.
+ *             j * tok_stride + h * d + i, j < n_new <= 2^28; strides in elements, multiples of 8.
  *   add       device int32 [n_seq], tokens that come to each sequence, 0 .. n_new (rows behind
  *             them are not read), or NULL: n_new to each. add[s] > len[s] is a length out of range.
  * Blocks that become full are written to their pages, tokens of the last one to the open block. */
@@ -361,7 +361,7 @@ int tq_b8_append(const tq_b8_cache* cache, const void* k, const void* v, tq_dtyp
                  void* stream);
 
 /* Hands the last n_tok tokens of every sequence back as values: row j of sequence s is the token
- * at position len[s] - n_tok + j. k, v: device, dtype [n_seq, n_tok, n_kv, d], 16-byte aligned.
+ * at position len[s] - n_tok + j; n_tok <= 2^28. k, v: device, dtype [n_seq, n_tok, n_kv, d], 16-byte aligned.
  * Rows before a sequence's first token, and of pages outside the pool, are left as they were. */
 int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dtype dtype, void* ws,
                size_t ws_bytes, void* stream);
@@ -399,7 +399,7 @@ int tq_b8_attention(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, i
  * The first n_first and the last n_last of them are always chosen, then those of the largest
  * score, ties to the lowest number.
  *   q, n_q, g as in tq_b8_attention; 0 <= n_first, n_last; n_first + n_last <= n_sel.
- *   sel       device int32 [n_seq, n_q, n_kv, n_sel]: ascending, filled up with -1.
+ *   sel       device int32 [n_seq, n_q, n_kv, n_sel], n_sel 1 .. 2^23: ascending, filled up with -1.
  *   ws        tq_b8_workspace_bytes(cache, n_q, g, n_sel, 0) bytes.                       */
 int tq_b8_select(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int n_q, int g, int n_first, int n_last,
                  int n_sel, int32_t* sel, void* ws, size_t ws_bytes, void* stream);
@@ -412,7 +412,7 @@ int tq_b8_select(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int 
  * and its codes are rint(code * (s_t / s')), scales and quotients in fp32. A block that is kept whole keeps
  * its bytes. The open block stays where it is.
  *   acc       device fp32 [n_seq, n_kv, 32 * max_blocks], as tq_b8_attention leaves it.
- *   keep_blocks  1 .. max_blocks, 32 * keep_blocks >= n_first + n_last.
+ *   keep_blocks  1 .. 2^23 (more than max_blocks: nothing is evicted), 32 * keep_blocks >= n_first + n_last.
  *   dst_table device int32 [n_seq, max_blocks], the pages that receive the kept blocks (the first
  *             keep_blocks entries are read). They must be other pages than those the table's
  *             full blocks name, of any sequence, except that a sequence with no more than

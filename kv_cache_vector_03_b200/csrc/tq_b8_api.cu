@@ -12,7 +12,7 @@
 namespace {
 
 static_assert(64 + kB8Counters <= TQ_STATUS_BYTES, "the arrival counts share the status word's bytes");
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23, kMaxRows = (int64_t)1 << 28;
 
 size_t align_up(size_t v) { return (v + TQ_ALIGN - 1) / TQ_ALIGN * TQ_ALIGN; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -94,7 +94,7 @@ size_t tq_b8_page_bytes(int d, int n_kv) {
 }
 
 size_t tq_b8_workspace_bytes(const tq_b8_cache* c, int n_q, int g, int n_sel, int weights) {
-    if (check_shape(c) != TQ_OK || n_q < 0 || g < 0 || n_sel < 0 || (int64_t)n_q * g > 16384) return 0;
+    if (check_shape(c) != TQ_OK || n_q < 0 || g < 0 || n_sel < 0 || n_sel > kMaxBlocks || (int64_t)n_q * g > 16384) return 0;
     return b8_ws(c, n_q, g, n_sel, weights != 0).total;
 }
 
@@ -104,7 +104,7 @@ int tq_b8_append(const tq_b8_cache* c, const void* k, const void* v, tq_dtype dt
     if (st != TQ_OK) return st;
     if (dtype != TQ_F32 && dtype != TQ_BF16) return TQ_ERR_ARG;
     if (n_new < 0 || seq_stride < 0 || tok_stride < 0 || seq_stride % 8 || tok_stride % 8) return TQ_ERR_ARG;
-    if (n_new > c->max_blocks * kB8Block) return TQ_ERR_ARG;   // no sequence can hold them
+    if (n_new > kMaxRows) return TQ_ERR_UNSUPPORTED;
     if (c->n_seq == 0 || n_new == 0) return TQ_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || (add && !aligned(add, 4))) return TQ_ERR_ARG;
     if ((st = check_ws(ws, ws_bytes, TQ_STATUS_BYTES)) != TQ_OK) return st;
@@ -124,7 +124,7 @@ int tq_b8_read(const tq_b8_cache* c, int64_t n_tok, void* k, void* v, tq_dtype d
     if (c->n_seq == 0 || n_tok == 0) return TQ_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return TQ_ERR_ARG;
     if ((st = check_ws(ws, ws_bytes, TQ_STATUS_BYTES)) != TQ_OK) return st;
-    if (n_tok > c->max_blocks * kB8Block) return TQ_ERR_ARG;
+    if (n_tok > kMaxRows) return TQ_ERR_UNSUPPORTED;
     B8ReadParams p;
     p.c = view(c, ws);
     p.n_tok = n_tok; p.k = k; p.v = v; p.dtype = dtype;
@@ -138,7 +138,7 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     if (st != TQ_OK) return st;
     if ((st = check_queries(q_dtype, n_q, g)) != TQ_OK) return st;
     if (!std::isfinite(scale) || !std::isfinite(decay)) return TQ_ERR_ARG;
-    if (n_sel < 0 || (n_sel > 0) != (sel != nullptr) || n_sel > c->max_blocks) return TQ_ERR_ARG;
+    if (n_sel < 0 || (n_sel > 0) != (sel != nullptr) || n_sel > kMaxBlocks) return TQ_ERR_ARG;
     if (acc_in && !acc_out) return TQ_ERR_ARG;
     if (sel && acc_out && n_q != 1) return TQ_ERR_UNSUPPORTED;
     if (c->n_seq == 0) return TQ_OK;
@@ -175,7 +175,7 @@ int tq_b8_select(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n_q,
     int st = check_cache(c);
     if (st != TQ_OK) return st;
     if ((st = check_queries(q_dtype, n_q, g)) != TQ_OK) return st;
-    if (n_first < 0 || n_last < 0 || n_sel < 1 || (int64_t)n_first + n_last > n_sel || n_sel > c->max_blocks)
+    if (n_first < 0 || n_last < 0 || n_sel < 1 || (int64_t)n_first + n_last > n_sel || n_sel > kMaxBlocks)
         return TQ_ERR_ARG;
     if (c->n_seq == 0) return TQ_OK;
     if (!q || !sel || !aligned(q, q_dtype == TQ_F32 ? 4 : 2) || !aligned(sel, 4)) return TQ_ERR_ARG;
@@ -194,7 +194,7 @@ int tq_b8_evict(const tq_b8_cache* c, const float* acc, int64_t keep_blocks, int
                 void* stream) {
     int st = check_cache(c);
     if (st != TQ_OK) return st;
-    if (keep_blocks < 1 || keep_blocks > c->max_blocks || n_first < 0 || n_last < 0 ||
+    if (keep_blocks < 1 || keep_blocks > kMaxBlocks || n_first < 0 || n_last < 0 ||
         n_first > keep_blocks * kB8Block || n_last > keep_blocks * kB8Block - n_first)
         return TQ_ERR_ARG;
     if (c->n_seq == 0) return TQ_OK;

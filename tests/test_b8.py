@@ -102,15 +102,17 @@ def test_append_and_read_refusals(lib):
     def append(k=0x1000, v=0x2000, dt=1, n=3, ss=4096, ts=1024, add=None, ws=0x100000, wb=256):
         return lib.lib.tq_b8_append(r, k, v, dt, n, ss, ts, add, ws, wb, None)
     for bad in (dict(k=None), dict(v=None), dict(k=0x1008), dict(v=0x2004), dict(dt=2), dict(n=-1), dict(ss=-8),
-                dict(ss=4), dict(ts=1020), dict(add=0x3002), dict(ws=None), dict(ws=0x100010), dict(n=513)):
+                dict(ss=4), dict(ts=1020), dict(add=0x3002), dict(ws=None), dict(ws=0x100010)):
         assert append(**bad) == lib.TQ_ERR_ARG, bad
     assert append(wb=255) == lib.TQ_ERR_WORKSPACE
+    assert append(n=(1 << 28) + 1) == lib.TQ_ERR_UNSUPPORTED
 
     def read(n=5, k=0x1000, v=0x2000, dt=1, ws=0x100000, wb=256):
         return lib.lib.tq_b8_read(r, n, k, v, dt, ws, wb, None)
-    for bad in (dict(n=-1), dict(n=513), dict(k=None), dict(k=0x1008), dict(v=None), dict(dt=7), dict(ws=None)):
+    for bad in (dict(n=-1), dict(k=None), dict(k=0x1008), dict(v=None), dict(dt=7), dict(ws=None)):
         assert read(**bad) == lib.TQ_ERR_ARG, bad
     assert read(wb=0) == lib.TQ_ERR_WORKSPACE
+    assert read(n=(1 << 28) + 1) == lib.TQ_ERR_UNSUPPORTED
 
 
 def test_attention_refusals(lib):
@@ -122,7 +124,7 @@ def test_attention_refusals(lib):
         return lib.lib.tq_b8_attention(r, q, dt, n_q, g, scale, sel, n_sel, ai, ao, decay, out, ws, wb, None)
     for bad in (dict(q=None), dict(q=0x1001), dict(dt=3), dict(n_q=0), dict(g=0), dict(scale=math.inf),
                 dict(scale=math.nan), dict(sel=0x3000), dict(n_sel=4), dict(sel=0x3002, n_sel=4), dict(n_sel=-1),
-                dict(sel=0x3000, n_sel=17), dict(ai=0x4000), dict(ao=0x4001), dict(decay=math.inf), dict(out=None),
+                dict(sel=0x3000, n_sel=(1 << 23) + 1), dict(ai=0x4000), dict(ao=0x4001), dict(decay=math.inf), dict(out=None),
                 dict(out=0x2008), dict(ws=None), dict(ws=0x100080)):
         assert call(**bad) == lib.TQ_ERR_ARG, bad
     assert call(n_q=128, g=129) == lib.TQ_ERR_UNSUPPORTED
@@ -144,13 +146,13 @@ def test_select_and_evict_refusals(lib):
     def select(q=0x1000, dt=1, n_q=1, g=4, nf=1, nl=1, n_sel=4, sel=0x2000, ws=0x100000, wb=1 << 40):
         return lib.lib.tq_b8_select(r, q, dt, n_q, g, nf, nl, n_sel, sel, ws, wb, None)
     for bad in (dict(q=None), dict(dt=9), dict(n_q=0), dict(g=-1), dict(nf=-1), dict(nl=-1), dict(nf=3, nl=2),
-                dict(n_sel=0), dict(n_sel=17), dict(nf=2 ** 31 - 1, nl=2 ** 31 - 1), dict(sel=None), dict(ws=None)):
+                dict(n_sel=0), dict(n_sel=(1 << 23) + 1), dict(nf=2 ** 31 - 1, nl=2 ** 31 - 1), dict(sel=None), dict(ws=None)):
         assert select(**bad) == lib.TQ_ERR_ARG, bad
     assert select(wb=lib.lib.tq_b8_workspace_bytes(r, 1, 4, 4, 0) - 1) == lib.TQ_ERR_WORKSPACE
 
     def evict(acc=0x1000, keep=4, nf=4, nl=32, dst=0x2000, kept=0x3000, lo=0x4000, ao=0x5000, ws=0x100000, wb=256):
         return lib.lib.tq_b8_evict(r, acc, keep, nf, nl, dst, kept, lo, ao, ws, wb, None)
-    for bad in (dict(acc=None), dict(keep=0), dict(keep=17), dict(nf=-1), dict(nl=-1), dict(nf=100, nl=29),
+    for bad in (dict(acc=None), dict(keep=0), dict(keep=(1 << 23) + 1), dict(nf=-1), dict(nl=-1), dict(nf=100, nl=29),
                 dict(nf=2 ** 62, nl=2 ** 62), dict(dst=None), dict(kept=None), dict(lo=None), dict(ao=None),
                 dict(lo=0x30000), dict(ao=0x1000), dict(kept=0x3001), dict(ws=None)):
         assert evict(**bad) == lib.TQ_ERR_ARG, bad
@@ -287,6 +289,7 @@ def test_append_bytes(m, d, n_kv, dtype):
     p = Pair(m, d, n_kv, 4, 12, 10 + d)
     for counts in ([1, 0, 31, 32], [1, 33, 1, 0], [30, 1, 0, 64], [33, 0, 95, 1], [0, 127, 1, 2], [1, 1, 1, 1]):
         p.append(counts, dtype, n_new=max(counts) + 3)
+    p.append([2, 0, 1, 0], dtype, n_new=32 * p.nb + 50)       # more rows than any sequence holds, few of them tokens
     assert p.ok()
     p.check_bytes()
 
@@ -353,7 +356,7 @@ def test_read(m, d, n_kv, dtype):
     p = Pair(m, d, n_kv, 4, 5, 20 + d)
     p.append([0, 31, 64, 133])
     td = torch.float32 if dtype == "f32" else torch.bfloat16
-    for n_tok in (1, 33, 160):
+    for n_tok in (1, 33, 160, 333):
         k, v = (torch.full((4, n_tok, n_kv, d), 768.0, dtype=td, device="cuda") for _ in range(2))
         m.tq_b8_read(p.cache, k, v, p.ws)
         for s, q in enumerate(p.seqs):
@@ -505,7 +508,7 @@ def test_attention_bad_pages_and_lengths(m):
 @pytest.mark.parametrize("d,n_kv,g,n_q,lens,n_sel,nf,nl,dtype", [
     (128, 2, 4, 1, [700, 90, 31], 5, 1, 1, "bf16"), (64, 3, 1, 1, [1500], 7, 0, 0, "f32"),
     (40, 1, 9, 3, [400, 66, 2], 4, 1, 2, "f32"), (256, 1, 8, 1, [640], 6, 2, 1, "bf16"),
-    (128, 1, 12, 2, [320, 321], 10, 0, 1, "bf16"), (8, 2, 2, 1, [999], 3, 1, 2, "f32")])
+    (128, 1, 12, 2, [320, 321], 10, 0, 1, "bf16"), (64, 2, 4, 1, [100, 31], 40, 1, 1, "bf16"), (8, 2, 2, 1, [999], 3, 1, 2, "f32")])
 def test_select_and_sparse_attention(m, d, n_kv, g, n_q, lens, n_sel, nf, nl, dtype):
     import torch
     p = Pair(m, d, n_kv, len(lens), -(-max(lens) // 32) + 2, 60 + d)
@@ -583,11 +586,11 @@ def test_sparse_attention_with_a_hand_made_selection(m):
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,n_kv,lens,keep,nf,nl", [
     (128, 3, [700, 64, 31, 0], 4, 4, 32), (64, 2, [1111], 9, 0, 0), (40, 1, [300, 333], 5, 160, 0),
-    (256, 2, [400], 7, 3, 50), (128, 1, [2000, 64], 1, 0, 32), (8, 2, [500], 15, 1, 1)])
+    (256, 2, [400], 7, 3, 50), (128, 1, [2000, 64], 1, 0, 32), (8, 2, [500], 15, 1, 1), (64, 1, [100, 70], 9, 4, 128)])
 def test_evict(m, d, n_kv, lens, keep, nf, nl):
     import torch
     nb = -(-max(lens) // 32) + 1
-    p = Pair(m, d, n_kv, len(lens), max(nb, keep), 80 + d, spare=len(lens) * max(nb, keep))
+    p = Pair(m, d, n_kv, len(lens), nb, 80 + d, spare=len(lens) * nb)
     p.append(lens)
     n_seq = len(lens)
     acc = torch.from_numpy(np.exp(2 * p.rng.standard_normal((n_seq, n_kv, 32 * p.nb))).astype(np.float32)).cuda()
