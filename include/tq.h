@@ -372,7 +372,7 @@ int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dty
  * A query whose position is negative, or that sees no token, gives zeros.
  *   q         device [n_seq, n_q, n_kv * g, d], fp32 or bf16, 16-byte aligned; n_q, g >= 1,
  *             n_q * g <= 16384. Blocks times query rows are limited too: with n_q * g (with sel, g) rows in
- *             tiles of 8 (16 above 8 rows, for d <= 128), sequences (with sel, times n_q) x kv heads x tiles x
+ *             tiles of 8, sequences (with sel, times n_q) x kv heads x tiles x
  *             (max_blocks + 1, or n_sel + 1) up to 2^30, else TQ_ERR_UNSUPPORTED.
  *   sel       device int32 [n_seq, n_q, n_kv, n_sel] block numbers from tq_b8_select: the query
  *             sees only tokens of these blocks and of the open block; entries outside the

@@ -102,7 +102,7 @@ struct B8EvictParams {
     float* acc_out;
 };
 
-int b8_attn_row_tile(int D, int rows);   // query rows a unit is computed for at once
+int b8_attn_row_tile(int D, int rows, int64_t blocks);   // query rows a unit is computed for at once
 int b8_attn_grid();                      // CTAs of one wave
 cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st);
 cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st);

@@ -60,7 +60,7 @@ B8Cache view(const tq_b8_cache* c, void* ws) {
 }
 
 // regions after the status word; a call uses those of its own kind, so they share the space
-struct B8Ws { size_t key, part, ml, lse, logits, total; int64_t logit_row; };
+struct B8Ws { size_t key, part, ml, lse, logits, total; int64_t logit_row; int rows, row_tile; };
 B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     B8Ws w = {};
     const size_t rows = (size_t)c->n_seq * c->n_kv * (size_t)n_q;
@@ -68,7 +68,10 @@ B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     w.key = off;
     const size_t select_end = align_up(off + (n_sel ? rows * (size_t)c->max_blocks * 4 : 0));
     w.logit_row = n_sel ? (int64_t)(n_sel + 1) * kB8Block : c->max_blocks * kB8Block;
-    const int tile = b8_attn_row_tile(b8_padded(c->d), n_sel ? g : n_q * g);
+    // rows and blocks of one virtual sequence (k_b8_attn.cu): of a sequence, with a selection of a query token
+    w.rows = n_sel ? g : n_q * g;
+    const int64_t blocks = c->n_seq * c->n_kv * (n_sel ? (int64_t)n_q * n_sel : c->max_blocks);
+    const int tile = w.row_tile = b8_attn_row_tile(b8_padded(c->d), w.rows, blocks);
     const size_t slots = rows && g ? 2 * (size_t)b8_attn_grid() * tile : 0;
     w.part = off; off = align_up(off + slots * b8_padded(c->d) * 4);
     w.ml = off; off = align_up(off + slots * 8);
@@ -165,8 +168,8 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     p.part_ml = reinterpret_cast<float*>(wsb + W.ml);
     p.count = reinterpret_cast<uint32_t*>(wsb) + 16;
     p.grid = b8_attn_grid();
-    p.row_tile = b8_attn_row_tile(p.c.D, sel ? g : n_q * g);
-    p.row_tiles = ((sel ? g : n_q * g) + p.row_tile - 1) / p.row_tile;
+    p.row_tile = W.row_tile;
+    p.row_tiles = (W.rows + p.row_tile - 1) / p.row_tile;
     return cuda_status(b8_launch_attention(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -194,7 +194,7 @@ def test_binding_refuses_wrong_tensors(lib):
 class Pair:
     """The same cache in the library and in the reference."""
 
-    def __init__(self, m, d, n_kv, n_seq, max_blocks, seed, spare=0):
+    def __init__(self, m, d, n_kv, n_seq, max_blocks, seed, spare=0, width=None):
         import torch
         self.m, self.torch, self.rng = m, torch, np.random.default_rng(seed)
         self.d, self.n_kv, self.n_seq, self.nb = d, n_kv, n_seq, max_blocks
@@ -202,7 +202,11 @@ class Pair:
         self.names = self.rng.permutation(n_pages).astype(np.int32)
         # pages nobody has written and the open block hold what would show: NaN scales, NaN tokens
         self.pages = torch.full((n_pages, m.tq_b8_page_bytes(d, n_kv)), 255, dtype=torch.uint8, device="cuda")
-        self.table = torch.from_numpy(self.names[:n_seq * max_blocks].reshape(n_seq, max_blocks).copy()).cuda()
+        table = self.names[:n_seq * max_blocks].reshape(n_seq, max_blocks)
+        if width is not None:                        # a longer table, whose further entries name no page
+            self.nb = width
+            table = np.concatenate([table, np.full((n_seq, width - max_blocks), -1, np.int32)], axis=1)
+        self.table = torch.from_numpy(table.copy()).cuda()
         self.length = torch.zeros(n_seq, dtype=torch.int32, device="cuda")
         self.open_ = torch.full((n_seq, n_kv, 2, 32, d), float("nan"), dtype=torch.bfloat16, device="cuda")
         self.cache = m.Cache8(d, self.pages, self.table, self.length, self.open_)
@@ -380,9 +384,9 @@ CASES = [  # d, n_kv, g, n_q, lengths, dtype
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,n_kv,g,n_q,lens,dtype", CASES)
-def test_attention(m, d, n_kv, g, n_q, lens, dtype):
+def test_attention(m, d, n_kv, g, n_q, lens, dtype, width=None):
     import torch
-    p = Pair(m, d, n_kv, len(lens), -(-max(lens) // 32) + 1, 30 + d + g)
+    p = Pair(m, d, n_kv, len(lens), -(-max(lens) // 32) + 1, 30 + d + g, width=width)
     p.append(lens)
     q, q64 = p.queries(n_q, g, dtype)
     ws = p.workspace(n_q, g)
@@ -415,6 +419,15 @@ def test_attention(m, d, n_kv, g, n_q, lens, dtype):
         sums = weight.copy()
         sums[:, :old] += 0.75 * a[:, :old]
         assert np.all(np.abs(w[:, :n] - sums) <= rel * sums + 1e-30) and (w[:, n:] == 99.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,n_kv,g,n_q,lens,dtype", [
+    (128, 2, 4, 4, [0, 70, 1200, 33], "bf16"), (64, 2, 8, 2, [900, 31, 64, 1], "f32"), (96, 1, 5, 6, [500, 45], "f32"),
+    (40, 1, 1, 32, [129, 2000], "bf16"), (200, 1, 16, 1, [300], "bf16")])
+def test_attention_of_many_rows_over_wide_tables(m, d, n_kv, g, n_q, lens, dtype):
+    """16 query rows and more where the cache has room for much: two tiles of rows at a time."""
+    test_attention(m, d, n_kv, g, n_q, lens, dtype, width=32768 // n_kv)
 
 
 @pytest.mark.gpu
