@@ -925,18 +925,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 auto ml_at = [&](int x, int r) {                // maximum and sum of part x; then the factor instead
                     return reinterpret_cast<float2*>(p.part_ml + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * 2);
                 };
-                for (int r = w; r < 8 * NT && row0 + r < rows; r += NW) {
+                const int valid = min(8 * NT, rows - row0);
+                for (int r = w; r < valid; r += NW) {
+                    float2 ml[2];                               // of the first 64 parts; more are read twice
                     float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
-                    for (int x = c0 + lane; x <= c1; x += 32) top = fmaxf(top, __ldcg(ml_at(x, r)).x);
-                    top = tq_warp_max(top);
-#pragma unroll 1
-                    for (int x = c0 + lane; x <= c1; x += 32) {
-                        const float2 ml = __ldcg(ml_at(x, r));
-                        const float y = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : tq_exp2(ml.x - top);
-                        __stcg(&ml_at(x, r)->x, y);
-                        sum = y == 0.f ? sum : fmaf(ml.y, y, sum);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int x = c0 + lane + 32 * k;
+                        ml[k] = x <= c1 ? __ldcg(ml_at(x, r)) : make_float2(-INFINITY, 0.f);
+                        top = fmaxf(top, ml[k].x);
                     }
+#pragma unroll 1
+                    for (int x = c0 + lane + 64; x <= c1; x += 32) top = fmaxf(top, __ldcg(ml_at(x, r)).x);
+                    top = tq_warp_max(top);
+                    auto factor = [&](int x, float2 v) {
+                        const float y = v.x == -INFINITY ? (v.y == 0.f ? 0.f : NAN) : tq_exp2(v.x - top);
+                        __stcg(&ml_at(x, r)->x, y);
+                        sum = y == 0.f ? sum : fmaf(v.y, y, sum);
+                    };
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (c0 + lane + 32 * k <= c1) factor(c0 + lane + 32 * k, ml[k]);
+#pragma unroll 1
+                    for (int x = c0 + lane + 64; x <= c1; x += 32) factor(x, __ldcg(ml_at(x, r)));
                     sum = tq_warp_sum(sum);
                     if (lane == 0) {
                         s_sum[r] = sum;
@@ -944,28 +955,50 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     }
                 }
                 __syncthreads();
+                // 4 rows at a time: thread (part group, 4 channels) adds up every PG-th part, then the groups meet
+                constexpr int PG = NW * 32 / (D / 4);
+                static_assert(PG * 4 * D * 4 <= NW * 8 * NT * RS * 4, "the groups' sums fit where the warps' did");
+                const int pg = threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4) * 4;
 #pragma unroll 1
-                for (int t = threadIdx.x; t < min(8 * NT, rows - row0) * D; t += NW * 32) {   // 4 threads per (row, 4 channels)
-                    const int r = t / D, e = t % D / 4 * 4;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int x = c0 + (t & 3); x <= c1; x += 4) {
-                        const float y = __ldcg(&ml_at(x, r)->x);
-                        const float4 z = __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * D + e));
-                        if (y != 0.f) {
-                            a.x = fmaf(z.x, y, a.x); a.y = fmaf(z.y, y, a.y); a.z = fmaf(z.z, y, a.z); a.w = fmaf(z.w, y, a.w);
+                for (int r0 = 0; r0 < valid; r0 += 4) {
+                    float4 a[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) a[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int x = c0 + pg; x <= c1; x += PG) {
+                        float y[4];
+                        float4 z[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const bool there = r0 + r < valid;
+                            y[r] = there ? __ldcg(&ml_at(x, r0 + r)->x) : 0.f;
+                            z[r] = there ? __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r0 + r) * D + ch))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (y[r] != 0.f) {
+                                a[r].x = fmaf(z[r].x, y[r], a[r].x); a[r].y = fmaf(z[r].y, y[r], a[r].y);
+                                a[r].z = fmaf(z[r].z, y[r], a[r].z); a[r].w = fmaf(z[r].w, y[r], a[r].w);
+                            }
                     }
 #pragma unroll
-                    for (int d = 1; d < 4; d <<= 1) {
-                        a.x += __shfl_xor_sync(0xffffffffu, a.x, d); a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
-                        a.z += __shfl_xor_sync(0xffffffffu, a.z, d); a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+                    for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(s_o + ((size_t)pg * 4 + r) * D + ch) = a[r];
+                    __syncthreads();
+                    for (int t = threadIdx.x; t < D; t += NW * 32) {           // (row, 4 channels)
+                        const int r = t / (D / 4), e = t % (D / 4) * 4;
+                        if (r0 + r >= valid || e >= c.d) continue;
+                        float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int x = 0; x < PG; ++x) {
+                            const float4 z = *reinterpret_cast<const float4*>(s_o + ((size_t)x * 4 + r) * D + e);
+                            b.x += z.x; b.y += z.y; b.z += z.z; b.w += z.w;
+                        }
+                        const float inv = s_sum[r0 + r] == 0.f ? 0.f : 1.f / s_sum[r0 + r];
+                        *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r0 + r) * c.d + e) =
+                            make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv);
                     }
-                    if ((t & 3) == 0 && e < c.d) {
-                        const float inv = s_sum[r] == 0.f ? 0.f : 1.f / s_sum[r];
-                        *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r) * c.d + e) =
-                            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                    }
+                    __syncthreads();
                 }
                 __syncthreads();
             }
