@@ -31,6 +31,7 @@ constexpr int kMinUnits = 8;        // units a CTA takes at least, where segment
 constexpr int kStraddle = 24;
 constexpr int kSegment = 10;         // what a segment costs beside its units, in units
 constexpr int kWholeUnits = 32;      // segments up to here are not shared
+constexpr int kGroup = 16;           // parts that are joined at a time, where there are many
 constexpr int kAccTok = 256;
 
 // Two CTAs share an SM, so that one computes while the other starts or joins a segment. Warps and ring stages of
@@ -905,25 +906,45 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         }
         __syncthreads();                                  // s_o and the row sums are free again
         if (!whole) {
-            // The CTA that brings a segment's last part joins all of them, in their order. The arrival count of a
-            // segment is back at 0 after.
-            const int first = s_before + seg * (units + kSegment) + kSegment;
-            const int c0 = s_plan.c0 >= 0 ? s_plan.c0 : s_plan.owner(first);
-            const int c1 = s_plan.c0 >= 0 ? s_plan.c1 : s_plan.owner(first + units - 1);
-            if (threadIdx.x == 0) {
-                // The 4-bit fields of CTAs c0 .. c1 - 1 are this segment's alone: one counts up to 15 parts, and
-                // in 15 fields or more there is a whole 16-bit one.
-                const int parts = c1 - c0 + 1, bit = parts < 16 ? 4 * c0 : (4 * c0 + 15) & ~15, sh = bit & 31;
-                const uint32_t field = parts < 16 ? 15u : 65535u;
-                const uint32_t got = (atomic_add_acq_rel(p.count + (bit >> 5), 1u << sh) >> sh & field) + 1;
-                s_last = (int)got == parts;
-                if (s_last) atomicSub(p.count + (bit >> 5), got << sh);
-            }
-            __syncthreads();
-            if (s_last) {
+            // Joining the parts of CTAs c0 .. c1, in their order: the CTA that brings the last one does it. More than
+            // 3 kGroup parts are joined in groups of kGroup first, each by the last of its own, into the group's first
+            // part, and then the groups; so no CTA adds up more than 3 kGroup. (In one go, 296 parts of 8 rows at D = 256
+            // took 90 us.)
+            const int start = s_before + seg * (units + kSegment) + kSegment;
+            const int c0 = s_plan.c0 >= 0 ? s_plan.c0 : s_plan.owner(start);
+            const int c1 = s_plan.c0 >= 0 ? s_plan.c1 : s_plan.owner(start + units - 1);
+            const int parts = c1 - c0 + 1;
+            const bool two = parts > 3 * kGroup;
+#pragma unroll 1
+            for (int level = two ? 0 : 1; level < 2; ++level) {
+                const bool done = level == 1;
+                const int first = done ? c0 : c0 + ((int)blockIdx.x - c0) / kGroup * kGroup, step = done && two ? kGroup : 1;
+                const int count = !two ? parts : done ? (parts + kGroup - 1) / kGroup : min(kGroup, c1 - first + 1);
+                if (count == 1) continue;                 // (a group of one is its own sum)
+                if (threadIdx.x == 0) {
+                    // Arrival counts, back at 0 afterwards. The 4-bit fields of CTAs c0 .. c1 - 1 are this segment's alone:
+                    // one counts up to 15 parts; where there are more, the group's 15 or 16 fields hold two aligned
+                    // 16-bit ones, the first for the group (or all parts), the second for the groups.
+                    int bit = 4 * first;
+                    uint32_t field = 15u;
+                    if (count > 15 || (two && done)) {
+                        bit = ((bit + 15) & ~15) + (two && done ? 16 : 0);
+                        field = 65535u;
+                    }
+                    const int sh = bit & 31;
+                    const uint32_t got = (atomic_add_acq_rel(p.count + (bit >> 5), 1u << sh) >> sh & field) + 1;
+                    s_last = (int)got == count;
+                    if (s_last) atomicSub(p.count + (bit >> 5), got << sh);
+                }
+                __syncthreads();
+                if (!s_last) break;
                 __threadfence();
-                auto ml_at = [&](int x, int r) {                // maximum and sum of part x; then the factor instead
-                    return reinterpret_cast<float2*>(p.part_ml + ((2 * (size_t)x + (x == c0)) * 8 * NT + r) * 2);
+                auto slot_of = [&](int k) {                     // of part (or group) k
+                    const int x = first + k * step;
+                    return 2 * (size_t)x + (x == c0);
+                };
+                auto ml_at = [&](int k, int r) {                // its maximum and sum; then the factor instead
+                    return reinterpret_cast<float2*>(p.part_ml + (slot_of(k) * 8 * NT + r) * 2);
                 };
                 const int valid = min(8 * NT, rows - row0);
                 for (int r = w; r < valid; r += NW) {
@@ -931,12 +952,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     float top = -INFINITY, sum = 0.f;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int x = c0 + lane + 32 * k;
-                        ml[k] = x <= c1 ? __ldcg(ml_at(x, r)) : make_float2(-INFINITY, 0.f);
+                        const int x = lane + 32 * k;
+                        ml[k] = x < count ? __ldcg(ml_at(x, r)) : make_float2(-INFINITY, 0.f);
                         top = fmaxf(top, ml[k].x);
                     }
 #pragma unroll 1
-                    for (int x = c0 + lane + 64; x <= c1; x += 32) top = fmaxf(top, __ldcg(ml_at(x, r)).x);
+                    for (int x = lane + 64; x < count; x += 32) top = fmaxf(top, __ldcg(ml_at(x, r)).x);
                     top = tq_warp_max(top);
                     auto factor = [&](int x, float2 v) {
                         const float y = v.x == -INFINITY ? (v.y == 0.f ? 0.f : NAN) : tq_exp2(v.x - top);
@@ -945,13 +966,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     };
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (c0 + lane + 32 * k <= c1) factor(c0 + lane + 32 * k, ml[k]);
+                        if (lane + 32 * k < count) factor(lane + 32 * k, ml[k]);
 #pragma unroll 1
-                    for (int x = c0 + lane + 64; x <= c1; x += 32) factor(x, __ldcg(ml_at(x, r)));
+                    for (int x = lane + 64; x < count; x += 32) factor(x, __ldcg(ml_at(x, r)));
                     sum = tq_warp_sum(sum);
                     if (lane == 0) {
+                        s_top[r] = top;
                         s_sum[r] = sum;
-                        if (WT) lse[r] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+                        if (WT && done) lse[r] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
                     }
                 }
                 __syncthreads();
@@ -965,14 +987,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                     for (int r = 0; r < 4; ++r) a[r] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-                    for (int x = c0 + pg; x <= c1; x += PG) {
+                    for (int x = pg; x < count; x += PG) {
                         float y[4];
                         float4 z[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const bool there = r0 + r < valid;
                             y[r] = there ? __ldcg(&ml_at(x, r0 + r)->x) : 0.f;
-                            z[r] = there ? __ldcg(reinterpret_cast<const float4*>(p.part + ((2 * (size_t)x + (x == c0)) * 8 * NT + r0 + r) * D + ch))
+                            z[r] = there ? __ldcg(reinterpret_cast<const float4*>(p.part + (slot_of(x) * 8 * NT + r0 + r) * D + ch))
                                          : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
 #pragma unroll
@@ -987,7 +1009,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     __syncthreads();
                     for (int t = threadIdx.x; t < D; t += NW * 32) {           // (row, 4 channels)
                         const int r = t / (D / 4), e = t % (D / 4) * 4;
-                        if (r0 + r >= valid || e >= c.d) continue;
+                        if (r0 + r >= valid) continue;
                         float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int x = 0; x < PG; ++x) {
@@ -995,13 +1017,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                             b.x += z.x; b.y += z.y; b.z += z.z; b.w += z.w;
                         }
                         const float inv = s_sum[r0 + r] == 0.f ? 0.f : 1.f / s_sum[r0 + r];
-                        *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r0 + r) * c.d + e) =
-                            make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv);
+                        if (!done)
+                            *reinterpret_cast<float4*>(p.part + (slot_of(0) * 8 * NT + r0 + r) * D + e) = b;
+                        else if (e < c.d)
+                            *reinterpret_cast<float4*>(p.out + q_row(v, h, row0 + r0 + r) * c.d + e) =
+                                make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv);
                     }
                     __syncthreads();
                 }
+                if (!done && threadIdx.x < valid)
+                    __stcg(ml_at(0, threadIdx.x), make_float2(s_top[threadIdx.x], s_sum[threadIdx.x]));
                 __syncthreads();
             }
+            __syncthreads();
         }
         u += part;
         x0 += part;

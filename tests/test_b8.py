@@ -431,7 +431,8 @@ def test_attention_of_many_rows_over_wide_tables(m, d, n_kv, g, n_q, lens, dtype
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("d,n_seq,long", [(256, 200, 1100), (64, 300, 1100), (64, 300, 40), (128, 40, 1500), (128, 3, 6000)])
+@pytest.mark.parametrize("d,n_seq,long", [(256, 200, 1100), (64, 300, 1100), (64, 300, 40), (128, 40, 1500), (128, 3, 6000),
+                                           (128, 1, 9000), (256, 2, 20000), (64, 1, 80000)])
 def test_attention_many_ragged_sequences(m, d, n_seq, long):
     """Batches of more sequences than a warp, a block or the grid has members, with few long ones among short
     and empty ones, so that work is cut within and between sequences; the same bits every time."""
