@@ -1,22 +1,36 @@
 // Decode attention over the paged 8-bit cache (tq_b8_attention).
 //
-// Work is a list of units: a unit is one 32-token block of one (sequence, kv head, tile of query
-// rows), and a sequence's open block is its last unit. Query rows (query token, head of the
-// group) that share a kv head share its units, so codes are read once for up to 8 NT rows. The
-// list is laid out in memory by nobody: every CTA of one persistent wave sums the lengths, takes an
-// equal contiguous share and walks it, so batches of any mixture of lengths are balanced. A
-// segment (the units of one sequence, head and tile) that lies in one CTA is finished there; parts of
-// a segment go to the workspace and k_b8_merge joins them in order.
+// Mathematics. With key codes c_t (scale s), value codes v_t (scale u), l_t = s <q, c_t> scale log2(e) and a reference m,
+//   o = sum_t 2^(l_t - m) u v_t / sum_t 2^(l_t - m)
+// over 32-token blocks, m following the largest logit (online softmax; only when it is passed by 2^8, which changes
+// nothing but the exponents' range).
 //
-// A warp takes every kWarps-th unit of its CTA's share and streams pages through a ring of its own
-// in shared memory with bulk copies (64 D + 16 bytes a unit), the page numbers of 32 units ahead
-// in its lanes' registers. Products run on the fp16 tensor cores with tokens as the M dimension,
-// so 8 query rows cost one n-tile: S^T = K Q^T and O^T += V^T P^T. Codes become exact fp16 values by
-// a byte permute into 1024 + (code + 128) and one subtraction of 1152. q is scaled by a power of two per
-// row and split into fp16 pieces: one holds a bf16 q exactly, two hold 22 bits of an fp32 q. Weights
-// are split into two fp16 pieces too: one piece alone is off by 2^-12, which an fp32 output shows.
-// Scales multiply after the products: the key scale on the logits (as a product kept in two
-// floats, so that large logits lose nothing), the value scale on each block's partial sum.
+// Work is a list of units: a 32-token block, or 16 tokens of an open block, for one (sequence, kv head, tile of 8 or 16
+// query rows). Query rows (query token, head of the group) share their kv head's units, so codes are read once for a
+// tile. The list is written down nowhere: the CTAs of one wave each sum the lengths, take their share and walk it, so
+// lengths stay on the device (a captured graph follows them) and ragged batches are balanced. A segment is the units of
+// one sequence, head and tile; parts of a segment that lie in several CTAs are joined by the CTA that brings the last.
+//
+// Streams. Pages come by bulk copies (64 D + 16 bytes) into a ring of a CTA's stages, the warps taking units in turn;
+// every wait has a limit.
+//
+// Products, tokens as the M dimension so that 8 query rows cost one n-tile:
+//   S^T = K Q^T in int8: the stored bytes are unsigned, code + 128; q is scaled by a power of two per row to 22 bits and
+//     split into three int8 pieces; sums are exact in int32, start at -128 sum(q piece), and become floats through the
+//     bits of 1.5 * 2^23. No key is converted. (fp16 products of converted keys cost 170 instructions a unit where
+//     this costs 90.)
+//   O^T += V^T P^T in fp16: a byte permute into 1024 + (code + 128) and a subtraction of 1152 make exact fp16 codes. The
+//     weights are two fp16 pieces: one alone is off by 2^-12, which an fp32 result shows. Each block's sum is scaled by
+//     u into fp32 registers.
+// Key scale and softmax scale are one product kept in two floats, applied with one rounding next to m, so that a
+// logit of 30 loses no more than one of 1: results are off by 3e-7, an fp32 evaluation by 2e-6.
+//
+// What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 181 us,
+// 0.91 of the measured copy rate; 200 us in a long run at the power limit); for small ones the fixed chain launch, lengths,
+// page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of 32768: 26 us, 10 of them HBM);
+// instructions where 16 query rows share little data. A unit takes 683 warp instructions at 8 rows. The tensor pipes are
+// busy 15 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions suffice: at 8 to 16 rows a tile of 128
+// rows would be nearly empty.
 #include <algorithm>
 #include <cfloat>
 
@@ -27,15 +41,21 @@ namespace {
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kBias = 7.f;         // weights are kept as 2^(7 + logit - m): their small pieces stay normal in fp16
 constexpr float kSlack = 8.f;        // m follows the maximum once it is passed by 2^8: 2^(7 + 8) < 65504
-constexpr int kMinUnits = 8;        // units a CTA takes at least, where segments are shared
-constexpr int kStraddle = 24;
-constexpr int kSegment = 10;         // what a segment costs beside its units, in units
-constexpr int kWholeUnits = 32;      // segments up to here are not shared
+// units a CTA takes at least, where segments are shared (one sequence of 8192 tokens: with 4 21.2 us, 8 18.6; 16 ragged ones
+// of 1500: with 8 20.5 us, 16 28.7)
+constexpr int kMinUnits = 8;
+// segments up to here are not shared (one sequence of 1024 tokens: with 32 16.4 us, 16 14.4; of 500: 14.3 and 15.6; 16 ragged
+// ones of 600: 16.4 and 18.5)
+constexpr int kWholeUnits = 32;
+constexpr int kStraddle = 24;        // price of a cut inside a CTA's share, in units (10000 cycles)
+constexpr int kSegment = 10;         // what a segment costs beside its units, in units (8000 cycles)
 constexpr int kGroup = 16;           // parts that are joined at a time, where there are many
-constexpr int kAccTok = 256;
+constexpr int kAccTok = 256;        // threads of a CTA that adds up weights
 
-// Two CTAs share an SM, so that one computes while the other starts or joins a segment. Warps and ring stages of
-// one of them, and in how many rounds its warps' sums meet in shared memory.
+// Two CTAs share an SM, so that one computes while the other starts or joins a segment (one CTA of 16 warps: 205 us for
+// 64 x 8192; two of 8: 199). Warps and ring stages of one of them, and in how many rounds its warps' sums meet in shared
+// memory. Warps: as many as spill next to nothing (64 x 8192 at D = 128, 8 rows: 6 warps 180 us, 7 with more spilled 199, 8
+// 193, and 4 or 5 no better than 6; at D = 64 8 warps 115 us, 6 125).
 constexpr int kCtasPerSm = 2;
 template <int D, int NT>
 struct Shape {
@@ -233,7 +253,8 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
             units = units_of(v0 + me);
             incl = scan(units * segs);
         }
-        const int here = one ? total : all, mine = units ? units + kSegment : 0, upto = scan(mine * segs), first = upto - mine * segs;
+        const int here = one ? total : all, mine = units ? units + kSegment : 0, upto = scan(mine * segs);
+        const int first = upto - mine * segs;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int u = (k ? hi : lo) - base_price;
@@ -345,7 +366,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, s = SP && p.n_q > 1 ? fv / p.n_q : fv;
             if (off >= pages) {
                 const uint16_t* k = b8_open(c, s, h, 0) + 16 * (off - pages) * c.d;
-                r = {reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(k + 32 * c.d), -2 - (off - pages), n >> 5};
+                r = {reinterpret_cast<const uint8_t*>(k), reinterpret_cast<const uint8_t*>(k + 32 * c.d), -2 - (off - pages),
+                     n >> 5};
             } else {
                 r.block = SP ? p.sel[((int64_t)fv * c.n_kv + h) * p.n_sel + off] : off;
                 if (r.block >= 0 && r.block < (n >> 5)) {
@@ -392,7 +414,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     // ldmatrix: lane l gives the row address of token l mod 16, chunk l / 16 (of a pair; pair x is 32 x bytes on, an
     // exclusive or since the swizzle is one)
     const uint32_t at_k = (lane & 15) * D + (((lane >> 4) ^ b8_swz(lane & 15, D / 16)) << 4);
-    const uint32_t at_v0 = 32 * D + 2 * tq * D + ((vch ^ sv0) << 4) + vhalf, at_v1 = 32 * D + (2 * tq + 1) * D + ((vch ^ sv1) << 4) + vhalf;
+    const uint32_t at_v0 = 32 * D + 2 * tq * D + ((vch ^ sv0) << 4) + vhalf;
+    const uint32_t at_v1 = 32 * D + (2 * tq + 1) * D + ((vch ^ sv1) << 4) + vhalf;
     for (int u = 0; u < mine;) {
         int n, units;
 #pragma unroll 1
@@ -453,12 +476,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                         sum[z] += piece[z];
                     }
                 }
-                const int id = lane + 32 * k;             // channels 4 id .. + 3: k-step id / 8, register id / 4 mod 2, lane id mod 4
+                // channels 4 id .. + 3: k-step id / 8, register id / 4 mod 2, lane id mod 4
+                const int id = lane + 32 * k;
                 if (id < D / 4)
 #pragma unroll
                     for (int z = 0; z < 3; ++z)
-                        reinterpret_cast<uint32_t*>(s_q)[((((r >> 3) * 3 + z) * (D / 32) + (id >> 3)) * 32 + (r & 7) * 4 + (id & 3)) * 2 +
-                                                         (id >> 2 & 1)] = word[z];
+                        reinterpret_cast<uint32_t*>(s_q)[((((r >> 3) * 3 + z) * (D / 32) + (id >> 3)) * 32 + (r & 7) * 4 + (id & 3)) *
+                                                             2 + (id >> 2 & 1)] = word[z];
             }
 #pragma unroll
             for (int z = 0; z < 3; ++z) sum[z] = (int)__reduce_add_sync(0xffffffffu, sum[z]);
@@ -503,316 +527,323 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 lg = p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0) * p.logit_row +
                      (at < pages ? 32 * (int64_t)at : 32 * (int64_t)pages + 16 * (at - pages));
             }
-            if (WT && what == -1)
+            // (an open half is 16 tokens, and nothing only where a wait has run out)
+            if (WT && what == -1 && (off + i - u < (SP ? p.n_sel : n >> 5) || lane < 16))
                 for (int r = 0; r < 8 * NT && row0 + r < rows; ++r) lg[r * p.logit_row + lane] = -INFINITY;
             if (what != -1) {
-            float sc[2][NT][4];                           // S^T: tokens 16 mt + gq (+ 8), rows 2 tq, 2 tq + 1
-            const uint8_t* kp = smem + (size_t)st * SB;
-            const uint8_t* vp = kp + 32 * D;
-            float ks = 1.f, vs = 1.f;
-            const int half = -2 - what;                   // of the open block
-            const int left = what >= 0 ? 32 : min(16, (n & 31) - 16 * half), pos0 = what >= 0 ? 32 * b : 32 * b + 16 * half;
-            if (what >= 0) {
-                const float2 kv = *reinterpret_cast<const float2*>(kp + 64 * D);
-                ks = kv.x;
-                vs = kv.y;
-                int acc[3][2][NT][4];                     // [piece][token half]: the codes are unsigned, code + 128
+                float sc[2][NT][4];                           // S^T: tokens 16 mt + gq (+ 8), rows 2 tq, 2 tq + 1
+                const uint8_t* kp = smem + (size_t)st * SB;
+                const uint8_t* vp = kp + 32 * D;
+                float ks = 1.f, vs = 1.f;
+                const int half = -2 - what;                   // of the open block
+                const int left = what >= 0 ? 32 : min(16, (n & 31) - 16 * half), pos0 = what >= 0 ? 32 * b : 32 * b + 16 * half;
+                if (what >= 0) {
+                    const float2 kv = *reinterpret_cast<const float2*>(kp + 64 * D);
+                    ks = kv.x;
+                    vs = kv.y;
+                    int acc[3][2][NT][4];                     // [piece][token half]: the codes are unsigned, code + 128
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {        // 32 channels: chunks 2 x, 2 x + 1
-                    uint32_t k[2][4];
-                    const uint32_t ka = tq_smem_addr(kp) + (at_k ^ (32 * x));
-                    tq_ldsm_x4(ka, k[0][0], k[0][1], k[0][2], k[0][3]);
-                    tq_ldsm_x4(ka + 16 * D, k[1][0], k[1][1], k[1][2], k[1][3]);
+                    for (int x = 0; x < D / 32; ++x) {        // 32 channels: chunks 2 x, 2 x + 1
+                        uint32_t k[2][4];
+                        const uint32_t ka = tq_smem_addr(kp) + (at_k ^ (32 * x));
+                        tq_ldsm_x4(ka, k[0][0], k[0][1], k[0][2], k[0][3]);
+                        tq_ldsm_x4(ka + 16 * D, k[1][0], k[1][1], k[1][2], k[1][3]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int z = 0; z < 3; ++z) {
-                            const uint2 q = s_q[((nt * 3 + z) * (D / 32) + x) * 32 + lane];
+                            for (int z = 0; z < 3; ++z) {
+                                const uint2 q = s_q[((nt * 3 + z) * (D / 32) + x) * 32 + lane];
 #pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) {
-                                if (x == 0) {
-                                    const int2 y = *reinterpret_cast<const int2*>(&s_qsum[z][8 * nt + 2 * tq]);
-                                    mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y, y.x, y.y, y.x, y.y);
-                                } else {
-                                    mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y);
+                                for (int mt = 0; mt < 2; ++mt) {
+                                    if (x == 0) {
+                                        const int2 y = *reinterpret_cast<const int2*>(&s_qsum[z][8 * nt + 2 * tq]);
+                                        mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y, y.x, y.y, y.x,
+                                                 y.y);
+                                    } else {
+                                        mma_u8s8(acc[z][mt][nt], k[mt][0], k[mt][1], k[mt][2], k[mt][3], q.x, q.y);
+                                    }
                                 }
                             }
-                        }
-                }
+                    }
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {     // sums below 2^22: the low bits of 1.5 * 2^23 + sum
-                            const float x0 = __int_as_float(acc[0][mt][nt][e]) - 12582912.f;
-                            const float x1 = __int_as_float(acc[1][mt][nt][e]) - 12582912.f;
-                            const float x2 = __int_as_float(acc[2][mt][nt][e]) - 12582912.f;
-                            sc[mt][nt][e] = fmaf(x0, 65536.f, fmaf(x1, 256.f, x2));
-                        }
-            } else {
-                // 16 tokens of the open block in bf16; q put together again and split into bf16 pieces, which
-                // three hold. Rows behind the last token hold anything and count as zeros.
+                            for (int e = 0; e < 4; ++e) {     // sums below 2^22: the low bits of 1.5 * 2^23 + sum
+                                const float x0 = __int_as_float(acc[0][mt][nt][e]) - 12582912.f;
+                                const float x1 = __int_as_float(acc[1][mt][nt][e]) - 12582912.f;
+                                const float x2 = __int_as_float(acc[2][mt][nt][e]) - 12582912.f;
+                                sc[mt][nt][e] = fmaf(x0, 65536.f, fmaf(x1, 256.f, x2));
+                            }
+                } else {
+                    // 16 tokens of the open block in bf16; q put together again and split into bf16 pieces, which
+                    // three hold. Rows behind the last token hold anything and count as zeros.
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+                            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
 #pragma unroll 1
-                for (int y = 0; y < D / 16; ++y) {        // 4 channels e0 .. + 3
-                    const int e0 = 16 * y + 4 * tq;
-                    uint2 k0 = make_uint2(0u, 0u), k1 = k0;
-                    if (gq < left && e0 < c.d) k0 = *reinterpret_cast<const uint2*>(kp + (gq * c.d + e0) * 2);
-                    if (gq + 8 < left && e0 < c.d) k1 = *reinterpret_cast<const uint2*>(kp + ((gq + 8) * c.d + e0) * 2);
+                    for (int y = 0; y < D / 16; ++y) {        // 4 channels e0 .. + 3
+                        const int e0 = 16 * y + 4 * tq;
+                        uint2 k0 = make_uint2(0u, 0u), k1 = k0;
+                        if (gq < left && e0 < c.d) k0 = *reinterpret_cast<const uint2*>(kp + (gq * c.d + e0) * 2);
+                        if (gq + 8 < left && e0 < c.d) k1 = *reinterpret_cast<const uint2*>(kp + ((gq + 8) * c.d + e0) * 2);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float a[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int z = 0; z < 3; ++z) {
-                            const uint32_t word = reinterpret_cast<const uint32_t*>(s_q)[(((nt * 3 + z) * (D / 32) + (y >> 1)) * 32 + lane) * 2 + (y & 1)];
+                            for (int z = 0; z < 3; ++z) {
+                                const uint32_t word =
+                                    reinterpret_cast<const uint32_t*>(s_q)[(((nt * 3 + z) * (D / 32) + (y >> 1)) * 32 + lane) * 2 + (y & 1)];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) a[j] = fmaf(a[j], 256.f, (float)(int8_t)(word >> (8 * j)));
-                        }
+                                for (int j = 0; j < 4; ++j) a[j] = fmaf(a[j], 256.f, (float)(int8_t)(word >> (8 * j)));
+                            }
 #pragma unroll
-                        for (int pc = 0; pc < 3; ++pc) {
-                            const uint32_t b0 = pack_bf2(a[0], a[1]), b1 = pack_bf2(a[2], a[3]);
-                            a[0] -= bf_lo(b0); a[1] -= bf_hi(b0); a[2] -= bf_lo(b1); a[3] -= bf_hi(b1);
-                            mma_bf16(sc[0][nt], k0.x, k1.x, k0.y, k1.y, b0, b1);
+                            for (int pc = 0; pc < 3; ++pc) {
+                                const uint32_t b0 = pack_bf2(a[0], a[1]), b1 = pack_bf2(a[2], a[3]);
+                                a[0] -= bf_lo(b0); a[1] -= bf_hi(b0); a[2] -= bf_lo(b1); a[3] -= bf_hi(b1);
+                                mma_bf16(sc[0][nt], k0.x, k1.x, k0.y, k1.y, b0, b1);
+                            }
                         }
                     }
                 }
-            }
-            // logits, running maximum, weights
-            const bool masked = left < 32 || pos0 + 31 > all_see;
-            auto gone = [&](int nt, int e, int t) { return gq + 8 * t >= left || pos0 + gq + 8 * t > sees[nt][e]; };
-            float ga[NT][2], gb[NT][2], top[NT][2];
-            bool grown = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    ga[nt][e] = fh[nt][e] * ks;
-                    gb[nt][e] = fmaf(fh[nt][e], ks, -ga[nt][e]) + fl[nt][e] * ks;
-                    float y[4];                                              // of token gq + 8 t
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) y[t] = sc[t >> 1][nt][2 * (t & 1) + e] * ga[nt][e];
-                    if (masked) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            if (gone(nt, e, t)) y[t] = -INFINITY;
-                    }
-                    top[nt][e] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                    grown = grown || top[nt][e] > m[nt][e] + kSlack;
-                }
-            if (WT) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (row0 + 8 * nt + 2 * tq + e < rows)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                if (what >= 0 || t < 2) {
-                                    const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
-                                    lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] =
-                                        masked && gone(nt, e, t) ? -INFINITY : fmaf(raw, ga[nt][e], raw * gb[nt][e]);
-                                }
-            }
-            if (__any_sync(0xffffffffu, grown)) {
+                // logits, running maximum, weights
+                const bool masked = left < 32 || pos0 + 31 > all_see;
+                auto gone = [&](int nt, int e, int t) { return gq + 8 * t >= left || pos0 + gq + 8 * t > sees[nt][e]; };
+                float ga[NT][2], gb[NT][2], top[NT][2];
+                bool grown = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float t = fmaxf(m[nt][e], top[nt][e]);
+                        ga[nt][e] = fh[nt][e] * ks;
+                        gb[nt][e] = fmaf(fh[nt][e], ks, -ga[nt][e]) + fl[nt][e] * ks;
+                        float y[4];                                              // of token gq + 8 t
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-                        const float f = m[nt][e] == -INFINITY ? 0.f : tq_exp2(m[nt][e] - t);
-                        m[nt][e] = t;
-                        big = big || (fabsf(t) >= 65536.f && t != -INFINITY);
-                        l[nt][e] *= f;
+                        for (int t = 0; t < 4; ++t) y[t] = sc[t >> 1][nt][2 * (t & 1) + e] * ga[nt][e];
+                        if (masked) {
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            o[mt][nt][e] *= f;
-                            o[mt][nt][2 + e] *= f;
+                            for (int t = 0; t < 4; ++t)
+                                if (gone(nt, e, t)) y[t] = -INFINITY;
                         }
+                        top[nt][e] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                        grown = grown || top[nt][e] > m[nt][e] + kSlack;
                     }
-                big = __any_sync(0xffffffffu, big);
-            }
-            if (big) {
-                // Beyond 2^16 m itself is rounded by more than a weight could show: subtract the rounded logits,
-                // of which the largest is m exactly.
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                            const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                            x = __fadd_rn(__fsub_rn(__fmul_rn(x, ga[nt][e]), mm), kBias);
-                        }
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                            const float ref = kBias - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]);
-                            x = fmaf(x, ga[nt][e], fmaf(x, gb[nt][e], ref));
-                        }
-            }
-            if (masked) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            if (gone(nt, e, t)) sc[t >> 1][nt][2 * (t & 1) + e] = -INFINITY;
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                        x = tq_exp2(x);
-                        l[nt][e] += x;
-                    }
-            if (what >= 0) {
-                uint32_t pf[2][NT][2][2];                 // P^T as B fragments: [token half][n-tile][piece][register]
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
+                if (WT) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float a = sc[y][nt][2 * e], b2 = sc[y][nt][2 * e + 1];
-                            const uint32_t hi = pack_h2(a, b2);
-                            const float2 t = unpack_h2(hi);
-                            pf[y][nt][0][e] = transpose8(hi);
-                            pf[y][nt][1][e] = transpose8(pack_h2(a - t.x, b2 - t.y));
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            if (row0 + 8 * nt + 2 * tq + e < rows)
 #pragma unroll
-                for (int z = 0; z < VW / 2; ++z) {        // 8 channels of a lane at a time
-                    uint32_t vw[8][2];                    // tokens 16 y + 2 tq, + 1, + 8, + 9
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const uint2 a = *reinterpret_cast<const uint2*>(
-                            kp + (t & 1 ? at_v1 : at_v0) + (16 * (t >> 2) + 8 * (t >> 1 & 1)) * D + (z & 1) * 8 + (z >> 1) * 128);
-                        vw[t][0] = a.x; vw[t][1] = a.y;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float acc[2][NT][4];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t v0 = vw[4 * y][x], v1 = vw[4 * y + 1][x], v8 = vw[4 * y + 2][x], v9 = vw[4 * y + 3][x];
-                            const uint32_t l0 = __byte_perm(v0, v1, 0x5140), h0 = __byte_perm(v0, v1, 0x7362);
-                            const uint32_t l8 = __byte_perm(v8, v9, 0x5140), h8 = __byte_perm(v8, v9, 0x7362);
-                            const uint32_t a0 = codes_h2<0x4140>(l0), a1 = codes_h2<0x4342>(l0), a2 = codes_h2<0x4140>(l8),
-                                           a3 = codes_h2<0x4342>(l8);
-                            const uint32_t b0 = codes_h2<0x4140>(h0), b1 = codes_h2<0x4342>(h0), b2 = codes_h2<0x4140>(h8),
-                                           b3 = codes_h2<0x4342>(h8);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int pc = 0; pc < 2; ++pc) {
-                                    const uint32_t p0 = pf[y][nt][pc][0], p1 = pf[y][nt][pc][1];
-                                    if (y == 0 && pc == 0) {
-                                        mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1, 0.f, 0.f, 0.f, 0.f);
-                                        mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1, 0.f, 0.f, 0.f, 0.f);
-                                    } else {
-                                        mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1);
-                                        mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1);
+                                for (int t = 0; t < 4; ++t)
+                                    if (what >= 0 || t < 2) {
+                                        const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
+                                        lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] =
+                                            masked && gone(nt, e, t) ? -INFINITY : fmaf(raw, ga[nt][e], raw * gb[nt][e]);
                                     }
-                                }
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    float& y = o[2 * (2 * z + x) + j][nt][e];
-                                    y = fmaf(vs, acc[j][nt][e], y);
-                                }
-                    }
                 }
-            } else {
-                // open block: bf16 values, three bf16 pieces of the weights. A value that is not finite must
-                // not meet the zero weight of a row that does not see its token: then token by token.
-                bool wild = false;
-                for (int t = lane; t < left * c.d / 8; t += 32) {
-                    const uint4 a = reinterpret_cast<const uint4*>(vp)[t];
-                    const uint32_t u4[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        wild = wild || (u4[y] & 0x7f80u) == 0x7f80u || (u4[y] & 0x7f800000u) == 0x7f800000u;
-                }
-                if (!__any_sync(0xffffffffu, wild)) {
-                    uint32_t pf[NT][3][2];
+                if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float a = sc[0][nt][2 * e], b2 = sc[0][nt][2 * e + 1];
+                            float t = fmaxf(m[nt][e], top[nt][e]);
 #pragma unroll
-                            for (int pc = 0; pc < 3; ++pc) {
-                                const uint32_t t = pack_bf2(a, b2);
-                                a -= bf_lo(t);
-                                b2 -= bf_hi(t);
-                                pf[nt][pc][e] = transpose8(t);
+                            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                            const float f = m[nt][e] == -INFINITY ? 0.f : tq_exp2(m[nt][e] - t);
+                            m[nt][e] = t;
+                            big = big || (fabsf(t) >= 65536.f && t != -INFINITY);
+                            l[nt][e] *= f;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                o[mt][nt][e] *= f;
+                                o[mt][nt][2 + e] *= f;
                             }
                         }
+                    big = __any_sync(0xffffffffu, big);
+                }
+                if (big) {
+                    // Beyond 2^16 m itself is rounded by more than a weight could show: subtract the rounded logits,
+                    // of which the largest is m exactly.
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {            // 8 channels of a lane: m-tiles 4 x .. 4 x + 3
-                        uint32_t vw[4][4];
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                float& x = sc[t >> 1][nt][2 * (t & 1) + e];
+                                const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                                x = __fadd_rn(__fsub_rn(__fmul_rn(x, ga[nt][e]), mm), kBias);
+                            }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                float& x = sc[t >> 1][nt][2 * (t & 1) + e];
+                                const float ref = kBias - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]);
+                                x = fmaf(x, ga[nt][e], fmaf(x, gb[nt][e], ref));
+                            }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                if (gone(nt, e, t)) sc[t >> 1][nt][2 * (t & 1) + e] = -INFINITY;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
-                            const int tok = 2 * tq + (t & 1) + 8 * (t >> 1), ch = channel<D>(gq, 4 * x, 0);
-                            uint4 a = make_uint4(0u, 0u, 0u, 0u);
-                            if (tok < left && ch < c.d) a = *reinterpret_cast<const uint4*>(vp + (tok * c.d + ch) * 2);
-                            vw[t][0] = a.x; vw[t][1] = a.y; vw[t][2] = a.z; vw[t][3] = a.w;
+                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
+                            x = tq_exp2(x);
+                            l[nt][e] += x;
                         }
+                if (what >= 0) {
+                    uint32_t pf[2][NT][2][2];                 // P^T as B fragments: [token half][n-tile][piece][register]
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5410), a1 = __byte_perm(vw[0][j], vw[1][j], 0x7632);
-                            const uint32_t a2 = __byte_perm(vw[2][j], vw[3][j], 0x5410), a3 = __byte_perm(vw[2][j], vw[3][j], 0x7632);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int pc = 0; pc < 3; ++pc)
-                                    mma_bf16(o[4 * x + j][nt], a0, a1, a2, a3, pf[nt][pc][0], pf[nt][pc][1]);
-                        }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int t = 0; t < left; ++t)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float y0 = __shfl_sync(0xffffffffu, sc[0][nt][e], (t & 7) * 4 + tq);
-                                const float y1 = __shfl_sync(0xffffffffu, sc[0][nt][2 + e], (t & 7) * 4 + tq);
-                                const float pr = t < 8 ? y0 : y1;
-                                if (pr == 0.f) continue;
+                                const float a = sc[y][nt][2 * e], b2 = sc[y][nt][2 * e + 1];
+                                const uint32_t hi = pack_h2(a, b2);
+                                const float2 t = unpack_h2(hi);
+                                pf[y][nt][0][e] = transpose8(hi);
+                                pf[y][nt][1][e] = transpose8(pack_h2(a - t.x, b2 - t.y));
+                            }
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) {
-                                    const int ch = channel<D>(gq, mt, 0);
-                                    if (ch < c.d) {
-                                        const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vp + (t * c.d + ch) * 2);
-                                        o[mt][nt][e] = fmaf(pr, bf_lo(v2), o[mt][nt][e]);
-                                        o[mt][nt][2 + e] = fmaf(pr, bf_hi(v2), o[mt][nt][2 + e]);
+                    for (int z = 0; z < VW / 2; ++z) {        // 8 channels of a lane at a time
+                        uint32_t vw[8][2];                    // tokens 16 y + 2 tq, + 1, + 8, + 9
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            const uint2 a = *reinterpret_cast<const uint2*>(
+                                kp + (t & 1 ? at_v1 : at_v0) + (16 * (t >> 2) + 8 * (t >> 1 & 1)) * D + (z & 1) * 8 +
+                                (z >> 1) * 128);
+                            vw[t][0] = a.x; vw[t][1] = a.y;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float acc[2][NT][4];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t v0 = vw[4 * y][x], v1 = vw[4 * y + 1][x];
+                                const uint32_t v8 = vw[4 * y + 2][x], v9 = vw[4 * y + 3][x];
+                                const uint32_t l0 = __byte_perm(v0, v1, 0x5140), h0 = __byte_perm(v0, v1, 0x7362);
+                                const uint32_t l8 = __byte_perm(v8, v9, 0x5140), h8 = __byte_perm(v8, v9, 0x7362);
+                                const uint32_t a0 = codes_h2<0x4140>(l0), a1 = codes_h2<0x4342>(l0), a2 = codes_h2<0x4140>(l8),
+                                               a3 = codes_h2<0x4342>(l8);
+                                const uint32_t b0 = codes_h2<0x4140>(h0), b1 = codes_h2<0x4342>(h0), b2 = codes_h2<0x4140>(h8),
+                                               b3 = codes_h2<0x4342>(h8);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int pc = 0; pc < 2; ++pc) {
+                                        const uint32_t p0 = pf[y][nt][pc][0], p1 = pf[y][nt][pc][1];
+                                        if (y == 0 && pc == 0) {
+                                            mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1, 0.f, 0.f, 0.f, 0.f);
+                                            mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1, 0.f, 0.f, 0.f, 0.f);
+                                        } else {
+                                            mma_f16(acc[0][nt], a0, a1, a2, a3, p0, p1);
+                                            mma_f16(acc[1][nt], b0, b1, b2, b3, p0, p1);
+                                        }
                                     }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        float& y = o[2 * (2 * z + x) + j][nt][e];
+                                        y = fmaf(vs, acc[j][nt][e], y);
+                                    }
+                        }
+                    }
+                } else {
+                    // open block: bf16 values, three bf16 pieces of the weights. A value that is not finite must
+                    // not meet the zero weight of a row that does not see its token: then token by token.
+                    bool wild = false;
+                    for (int t = lane; t < left * c.d / 8; t += 32) {
+                        const uint4 a = reinterpret_cast<const uint4*>(vp)[t];
+                        const uint32_t u4[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            wild = wild || (u4[y] & 0x7f80u) == 0x7f80u || (u4[y] & 0x7f800000u) == 0x7f800000u;
+                    }
+                    if (!__any_sync(0xffffffffu, wild)) {
+                        uint32_t pf[NT][3][2];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float a = sc[0][nt][2 * e], b2 = sc[0][nt][2 * e + 1];
+#pragma unroll
+                                for (int pc = 0; pc < 3; ++pc) {
+                                    const uint32_t t = pack_bf2(a, b2);
+                                    a -= bf_lo(t);
+                                    b2 -= bf_hi(t);
+                                    pf[nt][pc][e] = transpose8(t);
                                 }
                             }
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x) {            // 8 channels of a lane: m-tiles 4 x .. 4 x + 3
+                            uint32_t vw[4][4];
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                const int tok = 2 * tq + (t & 1) + 8 * (t >> 1), ch = channel<D>(gq, 4 * x, 0);
+                                uint4 a = make_uint4(0u, 0u, 0u, 0u);
+                                if (tok < left && ch < c.d) a = *reinterpret_cast<const uint4*>(vp + (tok * c.d + ch) * 2);
+                                vw[t][0] = a.x; vw[t][1] = a.y; vw[t][2] = a.z; vw[t][3] = a.w;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5410);
+                                const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7632);
+                                const uint32_t a2 = __byte_perm(vw[2][j], vw[3][j], 0x5410);
+                                const uint32_t a3 = __byte_perm(vw[2][j], vw[3][j], 0x7632);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int pc = 0; pc < 3; ++pc)
+                                        mma_bf16(o[4 * x + j][nt], a0, a1, a2, a3, pf[nt][pc][0], pf[nt][pc][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int t = 0; t < left; ++t)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float y0 = __shfl_sync(0xffffffffu, sc[0][nt][e], (t & 7) * 4 + tq);
+                                    const float y1 = __shfl_sync(0xffffffffu, sc[0][nt][2 + e], (t & 7) * 4 + tq);
+                                    const float pr = t < 8 ? y0 : y1;
+                                    if (pr == 0.f) continue;
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt) {
+                                        const int ch = channel<D>(gq, mt, 0);
+                                        if (ch < c.d) {
+                                            const uint32_t v2 = *reinterpret_cast<const uint32_t*>(vp + (t * c.d + ch) * 2);
+                                            o[mt][nt][e] = fmaf(pr, bf_lo(v2), o[mt][nt][e]);
+                                            o[mt][nt][2 + e] = fmaf(pr, bf_hi(v2), o[mt][nt][2 + e]);
+                                        }
+                                    }
+                                }
+                    }
                 }
-            }
             }
             __syncwarp();                                 // every lane has read the stage
             issue(i + ST, st);
