@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
                 best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
                 const int b = b0 + gq + 8 * r;
                 if (tq == 0 && b < nb) {         // (a block's key is this lane's alone, in every round of heads)
-                    const uint32_t u = order_bits(best[r]);
+                    const uint32_t u = order_bits(best[r] + 0.f);   // a score that underflows from below is 0 too
                     key[b] = g0 ? max(key[b], u) : u;
                 }
             }

@@ -579,6 +579,25 @@ def test_select_ties_and_odd_queries(m):
 
 
 @pytest.mark.gpu
+def test_select_scores_that_underflow_are_ties(m):
+    """Block 0's score is negative and below the smallest fp32 number, the others' are 0: the lowest number wins."""
+    import torch
+    d = 64
+    p = Pair(m, d, 1, 1, 4, 73)
+    for x in (-(2.0 ** -99), 0.0, 0.0, 0.0):
+        k = np.full((32, 1, d), x, np.float32)
+        p.length += 32
+        m.tq_b8_append(p.cache, torch.from_numpy(k[None]).cuda(), torch.from_numpy(k[None]).cuda(), p.ws)
+        p.seqs[0].append(k, k)
+    ws = p.workspace(1, 1, 1)
+    q = torch.full((1, 1, 1, d), 2.0 ** -99, device="cuda")
+    sel = torch.full((1, 1, 1, 1), 77, dtype=torch.int32, device="cuda")
+    m.tq_b8_select(p.cache, q, sel, ws, n_first=0, n_last=0)
+    assert p.ok(ws) and sel.flatten().tolist() == [0]
+    assert ref.select(p.seqs[0], q.double().cpu().numpy().reshape(1, 1, 1, d), 1, 0, 0).flatten().tolist() == [0]
+
+
+@pytest.mark.gpu
 def test_sparse_attention_with_a_hand_made_selection(m):
     """Entries outside the full blocks are passed over; the order does not matter to the result's meaning."""
     import torch
