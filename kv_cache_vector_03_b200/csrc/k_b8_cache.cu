@@ -11,8 +11,8 @@
 // touches the open block. Bound by HBM: 64 x 512 tokens of 8 heads (d = 128, bf16), 203 MB in 40 us, 0.77 of the
 // measured copy rate.
 //
-// Read. Codes times scale, in the caller's layout: 727 MB (as many bf16 values as 32 sequences keep of 8192 tokens) in
-// 124 us, 0.89 of the measured copy rate.
+// Read. Codes times scale, in the caller's layout. Bound by HBM: 727 MB (32 sequences of up to 4127 tokens as bf16) in 109 us,
+// the measured copy rate; 64 x 543 tokens in 36 us.
 #include "k_b8.cuh"
 
 namespace {
@@ -20,6 +20,7 @@ namespace {
 constexpr float kRound = 12583040.f;     // 1.5 * 2^23 + 128
 constexpr int kAppendWarps = 4;
 constexpr int kReadWarps = 8;
+constexpr int kReadTok = 8;
 
 // 8 channels as bf16 pairs
 template <bool F32>
@@ -165,86 +166,82 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
     }
 }
 
-// One warp per (sequence, 4 tokens of one block, keys or values): a lane takes 16 channels of a head of all four
-// tokens at a time, so four 16-byte loads are under way, and writes 32 or 64 bytes of each.
+// One warp per (sequence, kReadTok tokens of one block, keys or values, 32 pieces of the heads): a lane takes a piece of
+// one head, 16 bytes of the result, for all these tokens, so that that many loads are under way and a warp's stores are
+// contiguous. (A lane with 16 channels of 4 tokens, whose stores leave gaps for the next, and a warp for all heads in turn:
+// 124 us instead of 109 for 727 MB, 6.7 instead of 4.9 for 64 x 32 tokens.)
 template <int D, bool F32>
-__global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p, int64_t groups) {
+__global__ void __launch_bounds__(kReadWarps * 32) k_b8_read(const __grid_constant__ B8ReadParams p, int groups, int parts) {
+    constexpr int E = F32 ? 4 : 8;                       // channels of a piece
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
     const int lane = threadIdx.x & 31;
-    int64_t id = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
-    const int side = (int)(id & 1);
-    id >>= 1;
-    const int64_t s = id / groups;
-    if (s >= c.n_seq) return;
+    const uint32_t warp = blockIdx.x * kReadWarps + (threadIdx.x >> 5), id = warp / (uint32_t)parts;
+    const uint32_t i = (warp - id * parts) * 32 + lane, pieces = c.d / E;
+    const int side = (int)(id & 1), group = (int)(id >> 1);
+    if (group >= groups) return;
+    const int64_t s = blockIdx.y;
     const int n = b8_len(c, s);
     const int64_t from = max((int64_t)0, n - p.n_tok);
-    const int64_t pos = (from & ~(int64_t)3) + 4 * (id - s * groups);   // its tokens: pos .. pos + 3, from `from` to n
+    const int64_t pos = (from & ~(int64_t)(kReadTok - 1)) + kReadTok * (int64_t)group;   // up to n, its tokens pos, pos + 1, ...
     if (pos >= n) return;
-    const int b = (int)(pos >> 5), t0 = (int)(pos & 31), chunks = (c.d + 15) / 16;
+    const int b = (int)(pos >> 5), t0 = (int)(pos & 31);
     const bool paged = b < (n >> 5);
     uint8_t* page = nullptr;
     if (paged && !(page = b8_page(c, c.table[s * c.max_blocks + b]))) return;
-    const int64_t row0 = (s * p.n_tok + pos - (n - p.n_tok)) * c.n_kv * c.d;
+    if (i >= c.n_kv * pieces) return;
+    const int h = (int)(i / pieces), ch = (int)(i - h * pieces) * E;
+    const int64_t tok = (int64_t)c.n_kv * c.d;           // a token's values
+    const int64_t at = (s * p.n_tok + pos - (n - p.n_tok)) * tok + (int64_t)i * E;
     void* out = side ? p.v : p.k;
-    for (int i = lane; i < c.n_kv * chunks; i += 32) {
-        const int h = i / chunks, ch = i - h * chunks;
-        const bool both = 16 * ch + 8 < c.d;             // d may end in the middle of the 16 channels
-        if (paged) {
-            const float sc = *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side);
-            const uint8_t* codes = b8_codes(c, page, h, side);
-            uint4 w[4];
+    const int lo = (int)max((int64_t)0, from - pos), hi = (int)min((int64_t)kReadTok, n - pos);   // which of the tokens
+    if (paged) {
+        const float sc = *reinterpret_cast<const float*>(b8_entry(c, page, h) + 4 * side);
+        const uint8_t* codes = b8_codes(c, page, h, side) + (ch & 15);
+        uint32_t w[kReadTok][E / 4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                w[t] = tq_ldg_stream(codes + (t0 + t) * D + ((ch ^ b8_swz(t0 + t, D / 16)) << 4));
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (pos + t < from || pos + t >= n) continue;
-                const uint32_t u[4] = {w[t].x, w[t].y, w[t].z, w[t].w};
-                float f[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    f[k] = sc * (__uint_as_float(__byte_perm(u[k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f);
-                const int64_t at = row0 + (int64_t)t * c.n_kv * c.d + (int64_t)h * c.d + 16 * ch;
-                if (F32) {
-                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-                    o[0] = make_float4(f[0], f[1], f[2], f[3]);
-                    o[1] = make_float4(f[4], f[5], f[6], f[7]);
-                    if (both) {
-                        o[2] = make_float4(f[8], f[9], f[10], f[11]);
-                        o[3] = make_float4(f[12], f[13], f[14], f[15]);
-                    }
-                } else {
-                    __nv_bfloat162 r[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) r[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-                    o[0] = *reinterpret_cast<uint4*>(r);
-                    if (both) o[1] = *reinterpret_cast<uint4*>(r + 4);
-                }
+        for (int t = 0; t < kReadTok; ++t) {
+            const uint8_t* at_c = codes + (t0 + t) * D + (((ch >> 4) ^ b8_swz(t0 + t, D / 16)) << 4);
+            if (F32) {
+                w[t][0] = __ldcs(reinterpret_cast<const uint32_t*>(at_c));
+            } else {
+                const uint2 x = __ldcs(reinterpret_cast<const uint2*>(at_c));
+                w[t][0] = x.x;
+                w[t][E / 4 - 1] = x.y;
             }
-        } else {
+        }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (pos + t < from || pos + t >= n) continue;
-                const uint4* src = reinterpret_cast<const uint4*>(b8_open(c, s, h, side) + (t0 + t) * c.d + 16 * ch);
-                const int64_t at = row0 + (int64_t)t * c.n_kv * c.d + (int64_t)h * c.d + 16 * ch;
+        for (int t = 0; t < kReadTok; ++t) {
+            if (t < lo || t >= hi) continue;
+            float f[E];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k && !both) break;
-                    const uint4 x = src[k];
-                    if (F32) {
-                        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 8 * k);
-                        o[0] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
-                                           __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-                        o[1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
-                                           __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u));
-                    } else {
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + 8 * k) = x;
-                    }
-                }
+            for (int k = 0; k < E; ++k)
+                f[k] = sc * (__uint_as_float(__byte_perm(w[t][k >> 2], 0x4b000000u, 0x7440 + (k & 3))) - 8388736.f);
+            uint4 r;
+            if (F32) {
+                r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            } else {
+                __nv_bfloat162 y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __floats2bfloat162_rn(f[2 * k % E], f[(2 * k + 1) % E]);
+                r = *reinterpret_cast<uint4*>(y);
             }
+            reinterpret_cast<uint4*>(out)[(at + t * tok) / E] = r;
+        }
+    } else {
+        const uint16_t* src = b8_open(c, s, h, side) + t0 * c.d + ch;
+#pragma unroll
+        for (int t = 0; t < kReadTok; ++t) {
+            if (t < lo || t >= hi) continue;
+            uint4 r;
+            if (F32) {
+                const uint2 x = *reinterpret_cast<const uint2*>(src + t * c.d);
+                r = make_uint4(x.x << 16, x.x & 0xffff0000u, x.y << 16, x.y & 0xffff0000u);
+            } else {
+                r = *reinterpret_cast<const uint4*>(src + t * c.d);
+            }
+            reinterpret_cast<uint4*>(out)[(at + t * tok) / E] = r;
         }
     }
 }
@@ -268,8 +265,10 @@ cudaError_t b8_launch_append(const B8AppendParams& p, cudaStream_t st) {
 }
 
 cudaError_t b8_launch_read(const B8ReadParams& p, cudaStream_t st) {
-    const int64_t groups = (p.n_tok + 3) / 4 + 1;   // the first and the last may be cut
-    const int64_t grid = (p.c.n_seq * groups * 2 + kReadWarps - 1) / kReadWarps;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return B8_LAUNCH(k_b8_read, (unsigned)grid, kReadWarps, p, groups);
+    const int64_t groups = (p.n_tok + kReadTok - 1) / kReadTok + 1;   // the first and the last may be cut
+    const int parts = (p.c.n_kv * (p.c.d / (p.dtype ? 8 : 4)) + 31) / 32;
+    const int64_t warps = groups * 2 * parts;
+    if (warps > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)((warps + kReadWarps - 1) / kReadWarps), (unsigned)p.c.n_seq);
+    return B8_LAUNCH(k_b8_read, grid, kReadWarps, p, (int)groups, parts);
 }
