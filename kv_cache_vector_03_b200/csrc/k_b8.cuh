@@ -23,6 +23,34 @@ struct B8Cache {
     int n_kv, d, D;
 };
 
+// two fp32 operations in one instruction, each rounded as by itself
+TQ_DEVICE uint64_t f2_bits(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+TQ_DEVICE float2 f2_of(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+TQ_DEVICE float2 f2_fma(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return f2_of(r);
+}
+TQ_DEVICE float2 f2_add(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+TQ_DEVICE float2 f2_mul(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+TQ_DEVICE float2 f2(float a) { return make_float2(a, a); }
+
 TQ_DEVICE int b8_swz(int t, int chunks) { return ((t & 2) | (((t ^ (t >> 2)) & 1) << 2)) & (chunks - 1); }
 
 // a sequence's length, 0 (and the status flag) where it cannot be

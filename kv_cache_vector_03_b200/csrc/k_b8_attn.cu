@@ -25,8 +25,10 @@
 // Key scale and softmax scale are one product kept in two floats, applied with one rounding next to m, so that a
 // logit of 30 loses no more than one of 1: results are off by 3e-7, an fp32 evaluation by 2e-6.
 //
-// What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 181 us,
-// 0.91 of the measured copy rate; 200 us in a long run at the power limit); for small ones the fixed chain launch, lengths,
+// fp32 work goes two at a time (f2_*, rounded the same): 64 x 8192 181 -> 174 us.
+//
+// What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 174 us,
+// 0.94 of the measured copy rate; more in a long run at the power limit); for small ones the fixed chain launch, lengths,
 // page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of 32768: 26 us, 10 of them HBM);
 // instructions where 16 query rows share little data. A unit takes 683 warp instructions at 8 rows. The tensor pipes are
 // busy 15 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions suffice: at 8 to 16 rows a tile of 128
@@ -570,11 +572,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {     // sums below 2^22: the low bits of 1.5 * 2^23 + sum
-                                const float x0 = __int_as_float(acc[0][mt][nt][e]) - 12582912.f;
-                                const float x1 = __int_as_float(acc[1][mt][nt][e]) - 12582912.f;
-                                const float x2 = __int_as_float(acc[2][mt][nt][e]) - 12582912.f;
-                                sc[mt][nt][e] = fmaf(x0, 65536.f, fmaf(x1, 256.f, x2));
+                            for (int e = 0; e < 4; e += 2) {  // sums below 2^22: the low bits of 1.5 * 2^23 + sum
+                                float2 x[3];
+#pragma unroll
+                                for (int z = 0; z < 3; ++z)
+                                    x[z] = f2_add(make_float2(__int_as_float(acc[z][mt][nt][e]), __int_as_float(acc[z][mt][nt][e + 1])),
+                                                  f2(-12582912.f));
+                                const float2 y = f2_fma(x[0], f2(65536.f), f2_fma(x[1], f2(256.f), x[2]));
+                                sc[mt][nt][e] = y.x;
+                                sc[mt][nt][e + 1] = y.y;
                             }
                 } else {
                     // 16 tokens of the open block in bf16; q put together again and split into bf16 pieces, which
@@ -613,25 +619,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 // logits, running maximum, weights
                 const bool masked = left < 32 || pos0 + 31 > all_see;
                 auto gone = [&](int nt, int e, int t) { return gq + 8 * t >= left || pos0 + gq + 8 * t > sees[nt][e]; };
-                float ga[NT][2], gb[NT][2], top[NT][2];
+                float2 ga[NT], gb[NT];                        // of rows 2 tq, 2 tq + 1
+                float top[NT][2];
                 bool grown = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 f = make_float2(fh[nt][0], fh[nt][1]);
+                    ga[nt] = f2_mul(f, f2(ks));
+                    gb[nt] = f2_fma(make_float2(fl[nt][0], fl[nt][1]), f2(ks), f2_fma(f, f2(ks), make_float2(-ga[nt].x, -ga[nt].y)));
+                    float2 y[4];                                                 // of token gq + 8 t
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        ga[nt][e] = fh[nt][e] * ks;
-                        gb[nt][e] = fmaf(fh[nt][e], ks, -ga[nt][e]) + fl[nt][e] * ks;
-                        float y[4];                                              // of token gq + 8 t
+                    for (int t = 0; t < 4; ++t)
+                        y[t] = f2_mul(make_float2(sc[t >> 1][nt][2 * (t & 1)], sc[t >> 1][nt][2 * (t & 1) + 1]), ga[nt]);
+                    if (masked) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) y[t] = sc[t >> 1][nt][2 * (t & 1) + e] * ga[nt][e];
-                        if (masked) {
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                if (gone(nt, e, t)) y[t] = -INFINITY;
+                        for (int t = 0; t < 4; ++t) {
+                            if (gone(nt, 0, t)) y[t].x = -INFINITY;
+                            if (gone(nt, 1, t)) y[t].y = -INFINITY;
                         }
-                        top[nt][e] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                        grown = grown || top[nt][e] > m[nt][e] + kSlack;
                     }
+                    top[nt][0] = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
+                    top[nt][1] = fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y));
+                    grown = grown || top[nt][0] > m[nt][0] + kSlack || top[nt][1] > m[nt][1] + kSlack;
+                }
                 if (WT) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -643,7 +653,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                                     if (what >= 0 || t < 2) {
                                         const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
                                         lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] =
-                                            masked && gone(nt, e, t) ? -INFINITY : fmaf(raw, ga[nt][e], raw * gb[nt][e]);
+                                            masked && gone(nt, e, t) ? -INFINITY
+                                                                 : fmaf(raw, e ? ga[nt].y : ga[nt].x, raw * (e ? gb[nt].y : gb[nt].x));
                                     }
                 }
                 if (__any_sync(0xffffffffu, grown)) {
@@ -677,19 +688,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                             for (int t = 0; t < 4; ++t) {
                                 float& x = sc[t >> 1][nt][2 * (t & 1) + e];
                                 const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                                x = __fadd_rn(__fsub_rn(__fmul_rn(x, ga[nt][e]), mm), kBias);
+                                x = __fadd_rn(__fsub_rn(__fmul_rn(x, e ? ga[nt].y : ga[nt].x), mm), kBias);
                             }
                 } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 ref = make_float2(kBias - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]),
+                                                       kBias - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]));
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                                const float ref = kBias - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]);
-                                x = fmaf(x, ga[nt][e], fmaf(x, gb[nt][e], ref));
-                            }
+                        for (int t = 0; t < 4; ++t) {
+                            float* x = &sc[t >> 1][nt][2 * (t & 1)];
+                            const float2 v2 = make_float2(x[0], x[1]), y = f2_fma(v2, ga[nt], f2_fma(v2, gb[nt], ref));
+                            x[0] = y.x;
+                            x[1] = y.y;
+                        }
+                    }
                 }
                 if (masked) {
 #pragma unroll
@@ -703,13 +716,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            float& x = sc[t >> 1][nt][2 * (t & 1) + e];
-                            x = tq_exp2(x);
-                            l[nt][e] += x;
-                        }
+                    for (int t = 0; t < 4; ++t) {
+                        float* x = &sc[t >> 1][nt][2 * (t & 1)];
+                        x[0] = tq_exp2(x[0]);
+                        x[1] = tq_exp2(x[1]);
+                        const float2 y = f2_add(make_float2(l[nt][0], l[nt][1]), make_float2(x[0], x[1]));
+                        l[nt][0] = y.x;
+                        l[nt][1] = y.y;
+                    }
                 if (what >= 0) {
                     uint32_t pf[2][NT][2][2];                 // P^T as B fragments: [token half][n-tile][piece][register]
 #pragma unroll
@@ -720,9 +734,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                             for (int e = 0; e < 2; ++e) {
                                 const float a = sc[y][nt][2 * e], b2 = sc[y][nt][2 * e + 1];
                                 const uint32_t hi = pack_h2(a, b2);
-                                const float2 t = unpack_h2(hi);
+                                const float2 t = unpack_h2(hi), rest = f2_add(make_float2(a, b2), make_float2(-t.x, -t.y));
                                 pf[y][nt][0][e] = transpose8(hi);
-                                pf[y][nt][1][e] = transpose8(pack_h2(a - t.x, b2 - t.y));
+                                pf[y][nt][1][e] = transpose8(pack_h2(rest.x, rest.y));
                             }
 #pragma unroll
                     for (int z = 0; z < VW / 2; ++z) {        // 8 channels of a lane at a time
@@ -766,9 +780,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        float& y = o[2 * (2 * z + x) + j][nt][e];
-                                        y = fmaf(vs, acc[j][nt][e], y);
+                                    for (int e = 0; e < 4; e += 2) {
+                                        float* y = &o[2 * (2 * z + x) + j][nt][e];
+                                        const float2 v2 = f2_fma(f2(vs), make_float2(acc[j][nt][e], acc[j][nt][e + 1]),
+                                                                 make_float2(y[0], y[1]));
+                                        y[0] = v2.x;
+                                        y[1] = v2.y;
                                     }
                         }
                     }
