@@ -36,9 +36,8 @@ TQ_DEVICE uint4 load8(const void* base, int64_t elem) {
 }
 
 TQ_DEVICE uint32_t code2(uint32_t w, float inv) {   // two codes + 128 in the low two bytes
-    const float lo = fmaf(__uint_as_float(w << 16), inv, kRound);
-    const float hi = fmaf(__uint_as_float(w & 0xffff0000u), inv, kRound);
-    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
+    const float2 c = f2_fma(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), f2(inv), f2(kRound));
+    return __byte_perm(__float_as_uint(c.x), __float_as_uint(c.y), 0x0040);
 }
 TQ_DEVICE uint2 code8(uint4 x, float inv) {
     return make_uint2(__byte_perm(code2(x.x, inv), code2(x.y, inv), 0x5410),

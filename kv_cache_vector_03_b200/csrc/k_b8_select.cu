@@ -277,13 +277,13 @@ __global__ void __launch_bounds__(THREADS) k_b8_pick_tokens(const __grid_constan
                         WeightKey{p.acc + row * p.c.max_blocks * 32}, p.kept + row * 32 * p.keep_blocks);
 }
 
-// max(|c|) over the bytes c + 128 of a word, in the larger of two 16-bit halves: lo and hi run over words
+// the range of bytes c + 128, word by word
 struct ByteRange {
-    uint32_t lo, hi;                                 // 16-bit minima and maxima of the even and odd bytes
+    uint32_t lo = 0x00ff00ffu, hi = 0u;              // 16-bit minima and maxima of the even and odd bytes
     TQ_DEVICE void take(uint32_t w) {
         const uint32_t e = w & 0x00ff00ffu, o = __byte_perm(w, 0, 0x4341);
-        lo = __vminu2(lo, __vminu2(e, o));
-        hi = __vmaxu2(hi, __vmaxu2(e, o));
+        lo = __vimin3_u16x2(lo, e, o);
+        hi = __vimax3_u16x2(hi, e, o);
     }
     TQ_DEVICE int top() const {                      // the largest |c|
         const int l = (int)min(lo & 0xffffu, lo >> 16), h = (int)max(hi & 0xffffu, hi >> 16);
@@ -294,13 +294,14 @@ struct ByteRange {
 // One warp per (sequence, new block, head), keys and values together where the registers hold both (D <= 128): gathers
 // 32 kept tokens, finds the new scales, requantizes by one multiply-add per code and writes the block, its scales and
 // summary. The warps of new block keep_blocks move what belongs to the open block: its acc, the length.
-// Bound by instructions and by the chain kept -> table -> rows, all rows of a warp under way at once: 500 MB in 117 us
-// (32 sequences of up to 8192 tokens to half), 0.65 of the measured copy rate, issue slots 54 % busy. A lane holds 16 channels
+// Bound by the chain kept -> table -> rows (all rows of a warp under way at once) and by instructions: 500 MB in 104 us
+// (32 sequences of up to 8192 tokens to half), 0.73 of the measured copy rate. Registers are held to four CTAs an SM: with
+// three 117 us, with five (spilled) 104. A lane holds 16 channels
 // of D / 16 tokens; codes stay packed but for the multiply-add, maxima and the summary's ranges are taken on 16-bit pairs.
 template <int D>
 struct MoveSides { static constexpr int n = D == 256 ? 1 : 2; };
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_constant__ B8EvictParams p) {
+__global__ void __launch_bounds__(kMoveWarps * 32, 4) k_b8_move(const __grid_constant__ B8EvictParams p) {
     constexpr int CH = D / 16, TPI = 32 / CH, IT = CH;   // 16-byte chunks of a row; tokens per step; steps
     constexpr int NS = MoveSides<D>::n;
     const B8Cache& c = p.c;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
         top[y] = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            ByteRange br = {0x00ff00ffu, 0u};
+            ByteRange br;
             br.take(x[y][i].x);
             br.take(x[y][i].y);
             br.take(x[y][i].z);
@@ -382,12 +383,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_b8_move(const __grid_consta
             uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float f[4];
+                float2 f[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    f[k] = fmaf(__uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + k)) - 8388736.f, rt, kRound);
-                o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
-                                   __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
+                for (int k = 0; k < 2; ++k)
+                    f[k] = f2_fma(f2_add(make_float2(__uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7440 + 2 * k)),
+                                                     __uint_as_float(__byte_perm(u[q], 0x4b000000u, 0x7441 + 2 * k))),
+                                         f2(-8388736.f)),
+                                  f2(rt), f2(kRound));
+                o[q] = __byte_perm(__byte_perm(__float_as_uint(f[0].x), __float_as_uint(f[0].y), 0x0040),
+                                   __byte_perm(__float_as_uint(f[1].x), __float_as_uint(f[1].y), 0x0040), 0x5410);
                 if (side == 0) {
                     const uint32_t ev = o[q] & 0x00ff00ffu, od = __byte_perm(o[q], 0, 0x4341);
                     lo[2 * q] = __vminu2(lo[2 * q], ev);
