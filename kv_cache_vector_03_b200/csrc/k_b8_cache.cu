@@ -22,17 +22,27 @@ constexpr int kAppendWarps = 4;
 constexpr int kReadWarps = 8;
 constexpr int kReadTok = 8;
 
-// 8 channels as bf16 pairs
-template <bool F32>
-TQ_DEVICE uint4 load8(const void* base, int64_t elem) {
-    if (!F32) return tq_ldg_stream(static_cast<const uint16_t*>(base) + elem);
-    const uint4 a = tq_ldg_stream(static_cast<const float*>(base) + elem);
-    const uint4 b = tq_ldg_stream(static_cast<const float*>(base) + elem + 4);
+// past L1, of memory that this kernel may write later
+TQ_DEVICE uint4 load_once(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+// 8 fp32 channels as bf16 pairs
+TQ_DEVICE uint4 round8(uint4 a, uint4 b) {
     const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(__uint_as_float(a.x), __uint_as_float(a.y)),
                                  __floats2bfloat162_rn(__uint_as_float(a.z), __uint_as_float(a.w)),
                                  __floats2bfloat162_rn(__uint_as_float(b.x), __uint_as_float(b.y)),
                                  __floats2bfloat162_rn(__uint_as_float(b.z), __uint_as_float(b.w))};
     return *reinterpret_cast<const uint4*>(r);
+}
+template <bool F32>
+TQ_DEVICE uint4 load8(const void* base, int64_t elem) {
+    if (!F32) return tq_ldg_stream(static_cast<const uint16_t*>(base) + elem);
+    return round8(tq_ldg_stream(static_cast<const float*>(base) + elem), tq_ldg_stream(static_cast<const float*>(base) + elem + 4));
 }
 
 TQ_DEVICE uint32_t code2(uint32_t w, float inv) {   // two codes + 128 in the low two bytes
@@ -88,14 +98,29 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_b8_append(const __grid_co
     const bool in = ch * 8 < c.d;
     if (b < b1) {
         uint8_t* page = b8_page(c, c.table[s * c.max_blocks + b]);
+        // fp32 rows eight at a time, all their loads before the first is rounded (9 x 777 tokens, d = 80: 9.5 us instead
+        // of 14.3)
         uint4 x[CH];
+        constexpr int STEP = F32 && CH > 8 ? 8 : CH;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int t = t0 + i * TPI, pos = 32 * b + t;
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (in)
-                x[i] = pos < first ? *reinterpret_cast<const uint4*>(open + t * c.d + ch * 8)
-                                   : load8<F32>(src, row0 + (pos - first) * p.tok_stride + ch * 8);
+        for (int i0 = 0; i0 < CH; i0 += STEP) {
+            uint4 more[STEP];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                const int t = t0 + (i0 + i) * TPI, pos = 32 * b + t;
+                x[i0 + i] = more[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (in) {
+                    const bool old = pos < first;
+                    const int64_t at = row0 + (pos - first) * p.tok_stride + ch * 8;
+                    const uint4* from = reinterpret_cast<const uint4*>(
+                        old ? open + t * c.d + ch * 8 : static_cast<const uint16_t*>(src) + (F32 ? 2 * at : at));
+                    x[i0 + i] = load_once(from);
+                    if (F32 && !old) more[i] = load_once(from + 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < STEP; ++i)
+                if (F32 && 32 * b + t0 + (i0 + i) * TPI >= first) x[i0 + i] = round8(x[i0 + i], more[i]);
         }
         uint32_t m = 0u;
 #pragma unroll
