@@ -29,9 +29,9 @@
 //
 // What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 174 us,
 // 0.94 of the measured copy rate; more in a long run at the power limit); for small ones the fixed chain launch, lengths,
-// page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of 32768: 26 us, 10 of them HBM);
-// instructions where 16 query rows share little data. A unit takes 683 warp instructions at 8 rows. The tensor pipes are
-// busy 15 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions suffice: at 8 to 16 rows a tile of 128
+// page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of 32768: 25 us, 10 of them HBM);
+// instructions where 16 query rows share little data. A unit takes 619 warp instructions at 8 rows. The tensor pipes are
+// busy 16 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions suffice: at 8 to 16 rows a tile of 128
 // rows would be nearly empty.
 #include <algorithm>
 #include <cfloat>
