@@ -52,7 +52,7 @@ constexpr int kWholeUnits = 32;
 constexpr int kStraddle = 24;        // price of a cut inside a CTA's share, in units (10000 cycles)
 constexpr int kSegment = 10;         // what a segment costs beside its units, in units (8000 cycles)
 constexpr int kGroup = 16;           // parts that are joined at a time, where there are many
-constexpr int kAccTok = 256;        // threads of a CTA that adds up weights
+constexpr int kAccTok = 128;        // threads of a CTA that adds up weights (256 with 2 tokens each: 1 us more for 16 x 8100)
 
 // Two CTAs share an SM, so that one computes while the other starts or joins a segment (one CTA of 16 warps: 205 us for
 // 64 x 8192; two of 8: 199). Warps and ring stages of one of them, and in how many rounds its warps' sums meet in shared
@@ -141,7 +141,7 @@ struct Plan {
 // Sums the units of all virtual sequences and finds this CTA's share of them, one of three ways:
 //   short segments (up to kWholeUnits units), or so many that whole ones come out even: shares begin and end
 //     between segments, nothing is joined;
-//   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length. A CTA
+//   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length or evened out. A CTA
 //     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
 //     everyone would wait for it;
 //   else equal shares, cut where they fall. A segment is priced at its units and kSegment more, for what each begun
@@ -222,9 +222,23 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
     const bool whole = longest <= kWholeUnits ||
                        (n_segs > p.grid && (n_segs + p.grid - 1) / p.grid * longest <= total / p.grid + kStraddle);
     if (!whole && n_segs <= p.grid && one) {
-        // 1 + floor(units (grid - segments) / total) parts each are never more than the grid together
-        const int spare = min(p.grid, total / kMinUnits) - n_segs;
-        const int parts = units ? 1 + (spare > 0 ? (int)((uint32_t)units * (uint32_t)spare / (uint32_t)total) : 0) : 0;
+        // 1 + floor(units spare / total) parts each are never more than the grid together. Where that leaves parts well
+        // above the average and there are CTAs to spare: the smallest cap on a part's units that they can keep, to 1/64
+        // (30 ragged sequences of 2000: 33 us by the first rule, 29.7; the search itself costs 1 us).
+        const int spare = max(0, min(p.grid, total / kMinUnits) - n_segs), most = n_segs + spare;
+        int parts = units ? 1 + (int)((uint32_t)units * (uint32_t)spare / (uint32_t)total) : 0;
+        if (small && 8 * spare >= n_segs) {
+            int cap = (int)__reduce_max_sync(0xffffffffu, units ? (units + parts - 1) / parts : 0), low = total / most;
+            if (cap - low > kSegment) {
+#pragma unroll 1
+                while (cap - low > 1 + (cap >> 6)) {             // cap can be kept, low cannot
+                    const int mid = (low + cap) >> 1;
+                    if ((int)__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid * segs) <= most) cap = mid;
+                    else low = mid;
+                }
+                parts = (units + cap - 1) / cap;
+            }
+        }
         const int upto = scan(parts * segs), b = blockIdx.x;
         const bool far = units > parts * (total / p.grid + kStraddle);
         if (!(small ? __any_sync(0xffffffffu, far) : __syncthreads_or(far))) {
@@ -517,21 +531,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
 
+        // this lane's first logit of a row's first token, if logits are wanted
+        float* lg = WT ? p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0 + 2 * tq) * p.logit_row + gq : nullptr;
         for (; i < u + part; i += NW) {
             // The barrier's parity tells one phase from the next, not from the one after: unit i has to be the
             // stage's before its phase is waited for, since the warp that refills it may be far behind.
             for (uint32_t it = 0; ok && *const_cast<volatile int*>(&s_unit[st]) != i; ++it) ok = it < kWaitLimit;
             ok = __all_sync(0xffffffffu, ok && tq_mbar_wait(&s_full[st], phase, kWaitLimit));
             const int what = ok ? s_meta[st].x : -1, b = ok ? s_meta[st].y : 0;
-            float* lg = nullptr;                          // this unit's logits, [row][logit_row], if they are wanted
-            if (WT) {
-                const int at = off + i - u, pages = SP ? p.n_sel : n >> 5;
-                lg = p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0) * p.logit_row +
-                     (at < pages ? 32 * (int64_t)at : 32 * (int64_t)pages + 16 * (at - pages));
-            }
+            // where in a row of logits this unit's are
+            const int at = off + i - u, pages = SP ? p.n_sel : n >> 5, col = at < pages ? 32 * at : 32 * pages + 16 * (at - pages);
             // (an open half is 16 tokens, and nothing only where a wait has run out)
-            if (WT && what == -1 && (off + i - u < (SP ? p.n_sel : n >> 5) || lane < 16))
-                for (int r = 0; r < 8 * NT && row0 + r < rows; ++r) lg[r * p.logit_row + lane] = -INFINITY;
+            if (WT && what == -1 && (at < pages || lane < 16))
+                for (int r = 0; r < 8 * NT && row0 + r < rows; ++r)
+                    p.logits[(((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0 + r) * p.logit_row + col + lane] = -INFINITY;
             if (what != -1) {
                 float sc[2][NT][4];                           // S^T: tokens 16 mt + gq (+ 8), rows 2 tq, 2 tq + 1
                 const uint8_t* kp = smem + (size_t)st * SB;
@@ -644,18 +657,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 }
                 if (WT) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* to = lg + col + 8 * nt * p.logit_row;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (row0 + 8 * nt + 2 * tq + e < rows)
-#pragma unroll
-                                for (int t = 0; t < 4; ++t)
-                                    if (what >= 0 || t < 2) {
-                                        const float raw = sc[t >> 1][nt][2 * (t & 1) + e];
-                                        lg[(8 * nt + 2 * tq + e) * p.logit_row + gq + 8 * t] =
-                                            masked && gone(nt, e, t) ? -INFINITY
-                                                                 : fmaf(raw, e ? ga[nt].y : ga[nt].x, raw * (e ? gb[nt].y : gb[nt].x));
-                                    }
+                        for (int t = 0; t < 4; ++t) {
+                            const float2 raw = make_float2(sc[t >> 1][nt][2 * (t & 1)], sc[t >> 1][nt][2 * (t & 1) + 1]);
+                            float2 y = f2_fma(raw, ga[nt], f2_mul(raw, gb[nt]));
+                            if (masked && gone(nt, 0, t)) y.x = -INFINITY;
+                            if (masked && gone(nt, 1, t)) y.y = -INFINITY;
+                            if (what >= 0 || t < 2) {                            // (an open half is 16 tokens)
+                                if (row0 + 8 * nt + 2 * tq < rows) to[8 * t] = y.x;
+                                if (row0 + 8 * nt + 2 * tq + 1 < rows) to[p.logit_row + 8 * t] = y.y;
+                            }
+                        }
+                    }
                 }
                 if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -1093,7 +1108,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 // acc_out[t] = decay * acc_in[t] + sum over rows of 2^(logit - lse), rows in order: one thread adds up a token, so
 // nothing is added atomically. A thread has kAccPer tokens and takes four rows at a time, to have that many loads under
 // way. With a selection a table in shared memory says which of its entries holds a block.
-constexpr int kAccPer = 2, kAccTile = kAccTok * kAccPer;
+constexpr int kAccPer = 4, kAccTile = kAccTok * kAccPer;
 __global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int splits) {
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();

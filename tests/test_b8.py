@@ -457,6 +457,27 @@ def test_attention_many_ragged_sequences(m, d, n_seq, long):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,n_kv,g,lens", [
+    (64, 8, 2, [250 + (977 + 40503 * s) % 1751 for s in range(30)]),
+    (64, 6, 1, [0, 31] + [600 + (977 + 40503 * s) % 4301 for s in range(16)]),
+    (128, 2, 4, [100, 9000, 4000, 1700, 33])])
+def test_attention_parts_of_ragged_sequences(m, d, n_kv, g, lens):
+    """Fewer segments than the grid has CTAs, of lengths far apart, so that parts are evened out."""
+    import torch
+    p = Pair(m, d, n_kv, len(lens), -(-max(lens) // 32) + 1, 47)
+    p.append(lens)
+    q, q64 = p.queries(1, g, "bf16")
+    ws = p.workspace(1, g)
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    m.tq_b8_attention(p.cache, q, 0.1, out, ws)
+    assert p.ok(ws)
+    got = out.double().cpu().numpy().reshape(q64.shape)
+    for s, sq in enumerate(p.seqs):
+        want, _, size, reach = ref.attention(sq, q64[s], 0.1)
+        close(got[s], want, size, reach, d)
+
+
+@pytest.mark.gpu
 def test_attention_extremes(m):
     """Large logits of both signs, a negative scale, a zero query, a query that is not finite (its own
     row only), a tiny and a huge query."""
