@@ -34,42 +34,49 @@ TQ_DEVICE int candidates(int n, int n_q, int i) {
     return last < 0 ? 0 : min(n >> 5, (last >> 5) + 1);
 }
 
-// One CTA per row (sequence, query token, kv head) and range of blocks: its warps take 16 blocks each in turn; the first
-// summaries are on their way while the query heads become int8.
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int ranges, int range) {
+struct ScoreRow {
+    int s, h, nb;                                    // sequence, kv head, candidates
+    TQ_DEVICE ScoreRow(const B8SelectParams& p, int row) {
+        const int si = row / p.c.n_kv;
+        h = row - si * p.c.n_kv;
+        s = p.n_q == 1 ? si : si / p.n_q;
+        nb = candidates(b8_len(p.c, s), p.n_q, si - s * p.n_q);
+    }
+};
+
+// Scores of blocks from .. to - 1 of a row (sequence, query token, kv head) as ordered bits in key: a CTA's warps take 16
+// blocks each in turn, the first summaries on their way while the query heads become int8, with AHEAD (more registers) the
+// next ones while these are multiplied.
+template <int D, bool AHEAD>
+TQ_DEVICE void score(const B8SelectParams& p, int row, const ScoreRow& x, int from, int to, uint32_t* key) {
     constexpr int CH = D / 32;       // 16-byte chunks a lane takes of a summary's 2 D bytes
     constexpr int STEP = kScoreWarps * 16;
     const B8Cache& c = p.c;
-    tq_pdl_launch_dependents();
-    tq_pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int row = blockIdx.x / ranges, si = row / c.n_kv, h = row - si * c.n_kv, s = p.n_q == 1 ? si : si / p.n_q;
-    const int from = (blockIdx.x - row * ranges) * range;
-    const int nb = min(candidates(b8_len(c, s), p.n_q, si - s * p.n_q), from + range);
-    if (from >= nb) return;
     __shared__ uint32_t s_q[8][2 * D / 4 + 4];   // + 4 words: the 8 rows of a load fall on distinct banks
     __shared__ float s_step[8];
-    const int32_t* table = c.table + s * c.max_blocks;
-    uint32_t* key = p.key + row * c.max_blocks;
-    uint4 a[2][CH];                  // summaries and key scales of rows gq and gq + 8 of 16 blocks
-    float ks[2];
-    auto load = [&](int b0) {
+    const int32_t* table = c.table + x.s * c.max_blocks;
+    struct Part {                    // summaries and key scales of rows gq and gq + 8 of 16 blocks
+        uint4 a[2][CH];
+        float ks[2];
+    };
+    auto load = [&](Part& z, int b0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const uint8_t* e = nullptr;
-            if (b0 + gq + 8 * r < nb) {
+            if (b0 + gq + 8 * r < to) {
                 uint8_t* page = b8_page(c, table[b0 + gq + 8 * r]);
-                if (page) e = b8_entry(c, page, h);
+                if (page) e = b8_entry(c, page, x.h);
             }
-            ks[r] = e ? *reinterpret_cast<const float*>(e) : 0.f;
+            z.ks[r] = e ? *reinterpret_cast<const float*>(e) : 0.f;
 #pragma unroll
             for (int k = 0; k < CH; ++k)
-                a[r][k] = e ? *reinterpret_cast<const uint4*>(e + 32 + 16 * (tq + 4 * k)) : make_uint4(0u, 0u, 0u, 0u);
+                z.a[r][k] = e ? *reinterpret_cast<const uint4*>(e + 32 + 16 * (tq + 4 * k)) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
     for (int g0 = 0; g0 < p.g; g0 += 8) {        // 8 query heads at a time
-        load(from + 16 * w);
+        Part z;
+        load(z, from + 16 * w);
         if (g0) __syncthreads();
         {   // warp w holds query head g0 + w as int8: negative parts against lo, positive ones against hi
             const int j = g0 + w;
@@ -96,34 +103,48 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_cons
             if (lane == 0) s_step[w] = live ? am * kB8Inv127 : 0.f;
         }
         __syncthreads();
-        for (int b0 = from + 16 * w; b0 < nb; b0 += STEP) {
-            if (b0 != from + 16 * w) load(b0);
+        for (int b0 = from + 16 * w; b0 < to; b0 += STEP) {
+            Part next;
+            if (AHEAD && b0 + STEP < to) load(next, b0 + STEP);
             int acc[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 const uint32_t* b = &s_q[gq][4 * (tq + 4 * k)];
-                tq_imma(acc, a[0][k].x, a[1][k].x, a[0][k].y, a[1][k].y, b[0], b[1]);
-                tq_imma(acc, a[0][k].z, a[1][k].z, a[0][k].w, a[1][k].w, b[2], b[3]);
+                tq_imma(acc, z.a[0][k].x, z.a[1][k].x, z.a[0][k].y, z.a[1][k].y, b[0], b[1]);
+                tq_imma(acc, z.a[0][k].z, z.a[1][k].z, z.a[0][k].w, z.a[1][k].w, b[2], b[3]);
             }
             float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {        // blocks gq, gq, gq + 8, gq + 8; heads 2 tq, 2 tq + 1
                 const int j = 2 * tq + (k & 1);
                 if (g0 + j < p.g)
-                    best[k >> 1] = fmaxf(best[k >> 1], __fmul_rn(__fmul_rn((float)acc[k], ks[k >> 1]), s_step[j]));
+                    best[k >> 1] = fmaxf(best[k >> 1], __fmul_rn(__fmul_rn((float)acc[k], z.ks[k >> 1]), s_step[j]));
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
                 best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
                 const int b = b0 + gq + 8 * r;
-                if (tq == 0 && b < nb) {         // (a block's key is this lane's alone, in every round of heads)
+                if (tq == 0 && b < to) {         // (a block's key is this lane's alone, in every round of heads)
                     const uint32_t u = order_bits(best[r] + 0.f);   // a score that underflows from below is 0 too
                     key[b] = g0 ? max(key[b], u) : u;
                 }
             }
+            if (AHEAD) z = next;
+            else if (b0 + STEP < to) load(z, b0 + STEP);
         }
     }
+}
+
+// One CTA per row and range of blocks. A row with no more candidates than places needs no scores.
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score(const __grid_constant__ B8SelectParams p, int ranges, int range) {
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
+    const int row = blockIdx.x / ranges, from = (blockIdx.x - row * ranges) * range;
+    const ScoreRow x(p, row);
+    const int to = min(x.nb, from + range);
+    if (from < to && x.nb > p.n_sel) score<D, false>(p, row, x, from, to, p.key + row * p.c.max_blocks);
 }
 
 // Ascending indices of the chosen of n: all of them if n <= k, else the first nf, the last nl and the
@@ -265,6 +286,21 @@ __global__ void __launch_bounds__(THREADS) k_b8_pick_blocks(const __grid_constan
     const int nb = candidates(b8_len(p.c, s), p.n_q, si - s * p.n_q);
     pick<THREADS, KEYS>(nb, p.n_sel, p.n_first, p.n_last, ScoreKey{p.key + row * p.c.max_blocks},
                         p.sel + (int64_t)row * p.n_sel);
+}
+
+// Scores and choice of a whole row in one CTA.
+constexpr int kFusedBlocks = 512;
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score_pick(const __grid_constant__ B8SelectParams p) {
+    __shared__ uint32_t s_key[kFusedBlocks];
+    tq_pdl_launch_dependents();
+    tq_pdl_wait();
+    const int row = blockIdx.x;
+    const ScoreRow x(p, row);
+    if (x.nb > p.n_sel) score<D, true>(p, row, x, 0, x.nb, s_key);
+    __syncthreads();
+    pick<kScoreWarps * 32, kFusedBlocks / (kScoreWarps * 32)>(x.nb, p.n_sel, p.n_first, p.n_last, ScoreKey{s_key},
+                                                             p.sel + (int64_t)row * p.n_sel);
 }
 
 template <int THREADS, int KEYS>
@@ -428,6 +464,16 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 4) k_b8_move(const __grid_con
 
 cudaError_t b8_launch_select(const B8SelectParams& p, cudaStream_t st) {
     const int64_t rows = p.c.n_seq * p.n_q * p.c.n_kv;
+    // One kernel for both where a row is a step or two of one CTA, or four and the rows alone fill the GPU: selection and
+    // attention of 16 sequences of 8000 tokens, 8 heads, 27 us instead of 30, 32 of 16384 45 and 48; but 8 of 16000
+    // 28.8 and 28.2, 16 of 32000 49 and 42.
+    if (p.c.max_blocks <= (rows >= tq_device_sms() ? kFusedBlocks : kFusedBlocks / 2)) {
+        if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+        return tq_launch_pdl(p.c.D == 64    ? k_b8_score_pick<64>
+                             : p.c.D == 128 ? k_b8_score_pick<128>
+                                            : k_b8_score_pick<256>,
+                             dim3((unsigned)rows), dim3(kScoreWarps * 32), 0, st, p);
+    }
     // Ranges of blocks: a step of 128 each, longer where that gives more than four waves of CTAs
     const int64_t steps = (p.c.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16), slots = 16 * (int64_t)tq_device_sms();
     const int64_t per = std::max<int64_t>(1, (rows * steps + slots - 1) / slots), ranges = (steps + per - 1) / per;

@@ -577,6 +577,25 @@ def test_select_and_sparse_attention(m, d, n_kv, g, n_q, lens, n_sel, nf, nl, dt
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,n_kv,g,n_q,lens,width,n_sel", [
+    (64, 2, 3, 1, [700, 2100, 64, 0], 300, 9), (128, 1, 9, 2, [4200], 300, 20), (256, 2, 4, 1, [1500, 900], 600, 3),
+    (40, 1, 1, 1, [9000], 300, 40), (64, 5, 2, 3, [330 + 97 * s for s in range(10)], 300, 8),
+    (128, 3, 1, 1, [40 + 31 * s for s in range(50)], 400, 12), (64, 1, 17, 1, [3300, 64], 104, 2)])
+def test_select_over_tables_of_several_widths(m, d, n_kv, g, n_q, lens, width, n_sel):
+    """Rows of few and of many blocks, few and many rows, and rows with no more blocks than are chosen."""
+    import torch
+    p = Pair(m, d, n_kv, len(lens), width, 76)
+    p.append(lens)
+    q, q64 = p.queries(n_q, g, "f32")
+    ws = p.workspace(n_q, g, n_sel)
+    sel = torch.full((len(lens), n_q, n_kv, n_sel), 77, dtype=torch.int32, device="cuda")
+    m.tq_b8_select(p.cache, q, sel, ws, n_first=1, n_last=1)
+    assert p.ok(ws)
+    for s, sq in enumerate(p.seqs):
+        assert np.array_equal(sel[s].cpu().numpy(), ref.select(sq, q64[s], n_sel, 1, 1)), s
+
+
+@pytest.mark.gpu
 def test_select_ties_and_odd_queries(m):
     """Equal blocks score the same: the lowest numbers win. A query of zeros, NaN or infinities scores 0."""
     import torch
