@@ -4,14 +4,15 @@
 // Score. For codes between lo_i and hi_i, sum_i qi_i code_i <= sum_i max(qi_i lo_i, qi_i hi_i) =
 // <min(qi, 0), lo> + <max(qi, 0), hi>: one int8 product of length 2 D with the block's summary,
 // exact in int32, on the int8 tensor cores (16 blocks x 8 heads per warp). A block costs 2 D + 4
-// bytes here where attention reads 64 D. Bound by the chain table -> summary: 16 x 512 blocks of 8 heads in 11.7 us.
+// bytes here where attention reads 64 D. Bound by the chain table -> summary: 16 x 512 blocks of 8 heads in 12.9 us
+// (80 registers, nothing spilled; held to 64, four CTAs an SM: 1 to 4 us more).
 //
 // Choice of the k largest of n. Keys are order-preserving 32-bit patterns. The k-th largest is
 // found digit by digit (11 + 11 + 10 bits, fewer once all keys with the digits so far are taken) from histograms in
 // shared memory; a last pass in index order writes what lies above it and the first of what equals it, by prefix sums,
 // so the result is ascending and ties go to the lowest index. A row is one CTA's, its keys in registers: a chain of
-// barriers: 256 rows of up to 512 blocks 6.3 us, 8 of 4096 7.3, 32 of up to 8192 tokens 12.6 (cold; both kernels of a
-// selection over 8 x 4096 blocks, overlapped: 10).
+// barriers: 8 rows of 4096 blocks 7.3 us, 32 of up to 8192 tokens 12.6 (cold; both kernels of a selection over 8 x 4096
+// blocks, overlapped: 10).
 #include <algorithm>
 #include <cfloat>
 
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(THREADS) k_b8_pick_blocks(const __grid_constan
                         p.sel + (int64_t)row * p.n_sel);
 }
 
-// Scores and choice of a whole row in one CTA.
+// Scores and choice of a whole row in one CTA: 160 rows of 512 blocks in 17 us cold, 256 of up to 512 in 14.8 warm.
 constexpr int kFusedBlocks = 512;
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) k_b8_score_pick(const __grid_constant__ B8SelectParams p) {
