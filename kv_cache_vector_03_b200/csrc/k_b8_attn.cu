@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
         s_unit[threadIdx.x] = -1;
     }
     tq_fence_mbar_init();
+    __syncthreads();                                 // every warp issues copies into the ring: it is set up by now
     tq_pdl_launch_dependents();
     tq_pdl_wait();                                   // nothing is read before the kernel in front is done
 
