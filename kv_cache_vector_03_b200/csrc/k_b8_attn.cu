@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                         a.x = fmaf(z.x, f, a.x); a.y = fmaf(z.y, f, a.y); a.z = fmaf(z.z, f, a.z); a.w = fmaf(z.w, f, a.w);
                     }
                 }
-                const uint32_t team = __activemask();
+                const uint32_t team = ((1u << G) - 1u) << (lane & ~(G - 1));   // they share r, so all of them come here
 #pragma unroll
                 for (int d = 1; d < G; d <<= 1) {
                     a.x += __shfl_xor_sync(team, a.x, d); a.y += __shfl_xor_sync(team, a.y, d);
