@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "b8_shares.h"
 #include "k_b8.cuh"
 
 namespace {
@@ -50,7 +51,6 @@ constexpr int kMinUnits = 8;
 // ones of 600: 16.4 and 18.5)
 constexpr int kWholeUnits = 32;
 constexpr int kStraddle = 24;        // price of a cut inside a CTA's share, in units (10000 cycles)
-constexpr int kSegment = 10;         // what a segment costs beside its units, in units (8000 cycles)
 constexpr int kGroup = 16;           // parts that are joined at a time, where there are many
 constexpr int kAccTok = 128;        // threads of a CTA that adds up weights (256 with 2 tokens each: 1 us more for 16 x 8100)
 
@@ -131,12 +131,7 @@ struct Plan {
     int virt, x;                 // from unit x of virtual sequence virt on
     int c0, c1;                  // the CTAs that share this CTA's only segment, or c0 = -1: ask owner()
     int before;                  // (then) the price of all virtual sequences before virt
-    int base, extra;             // equal shares: a price of base, one more for the first `extra` CTAs
-    TQ_DEVICE int share(int c) const { return c * base + min(c, extra); }
-    TQ_DEVICE int owner(int u) const {
-        const int wide = extra * (base + 1);
-        return u < wide ? u / (base + 1) : extra + (u - wide) / base;
-    }
+    B8Shares shares;             // (and) the equal shares
 };
 // Sums the units of all virtual sequences and finds this CTA's share of them, one of three ways:
 //   short segments (up to kWholeUnits units), or so many that whole ones come out even: shares begin and end
@@ -144,8 +139,8 @@ struct Plan {
 //   no more segments than CTAs: each segment is cut into parts, a CTA each, in proportion to its length or evened out. A CTA
 //     with parts of two segments would pay for a second start and end (about 5 us, kStraddle units), and
 //     everyone would wait for it;
-//   else equal shares, cut where they fall. A segment is priced at its units and kSegment more, for what each begun
-//     segment costs (its queries, the meeting of the warps), so that CTAs with many segments get fewer units.
+//   else equal shares of a price (b8_shares.h), cut where they fall. A begun segment costs its queries and the meeting
+//     of the warps beside its units.
 // Up to 32 virtual sequences: every warp for itself, a lane each; more: the block, a thread each, tile by tile.
 template <int THREADS, bool SP>
 TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) {
@@ -229,7 +224,7 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
         int parts = units ? 1 + (int)((uint32_t)units * (uint32_t)spare / (uint32_t)total) : 0;
         if (small && 8 * spare >= n_segs) {
             int cap = (int)__reduce_max_sync(0xffffffffu, units ? (units + parts - 1) / parts : 0), low = total / most;
-            if (cap - low > kSegment) {
+            if (cap - low > kB8Segment) {
 #pragma unroll 1
                 while (cap - low > 1 + (cap >> 6)) {             // cap can be kept, low cannot
                     const int mid = (low + cap) >> 1;
@@ -257,11 +252,10 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
         }
     }
     const int ctas = min(p.grid, whole ? min(total, n_segs) : max(1, total / kMinUnits));
-    const int price = total + kSegment * segs * filled;
-    pl.base = price / ctas;
-    pl.extra = price - pl.base * ctas;
+    pl.shares.make(total, segs * filled, ctas);
+    const int per = pl.shares.per, price = pl.shares.price(total, segs * filled);
     if ((int)blockIdx.x >= ctas) return;
-    const int lo = pl.share(blockIdx.x), hi = pl.share(blockIdx.x + 1);
+    const int lo = pl.shares.share(blockIdx.x), hi = pl.shares.share(blockIdx.x + 1);
     int4 start = make_int4(0, 0, 0, 0), end = make_int4(0, 0, total, 0);   // virtual sequence, its unit, units before, price before
 #pragma unroll 1
     for (int v0 = 0, base = 0, base_price = 0;; v0 += THREADS) {
@@ -269,14 +263,14 @@ TQ_DEVICE void make_plan(const B8AttnParams& p, int n_virt, int segs, Plan& pl) 
             units = units_of(v0 + me);
             incl = scan(units * segs);
         }
-        const int here = one ? total : all, mine = units ? units + kSegment : 0, upto = scan(mine * segs);
+        const int here = one ? total : all, mine = units ? units + per : 0, upto = scan(mine * segs);
         const int first = upto - mine * segs;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int u = (k ? hi : lo) - base_price;
             if (u < 0 || u >= all) continue;             // not in this tile
             const bool is = first <= u && u < upto;
-            const int seg = is ? (u - first) / mine : 0, off = is ? max(0, u - first - seg * mine - kSegment) : 0;
+            const int seg = is ? (u - first) / mine : 0, off = is ? max(0, u - first - seg * mine - per) : 0;
             const int x = seg * units + (whole ? 0 : off);
             (k ? end : start) = hand(is, k, v0 + me, x, base + incl - units * segs + x, base_price + first);
         }
@@ -438,7 +432,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll 1
         while (x0 >= (units = virt_units<SP>(p, v, n)) * segs && v + 1 < n_virt) {
             x0 -= units * segs;
-            if (threadIdx.x == 0 && units) s_before += (units + kSegment) * segs;
+            if (threadIdx.x == 0 && units) s_before += (units + s_plan.shares.per) * segs;
             ++v;
         }
         const int seg = x0 / units, off = x0 - seg * units;
@@ -974,9 +968,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             // 3 kGroup parts are joined in groups of kGroup first, each by the last of its own, into the group's first
             // part, and then the groups; so no CTA adds up more than 3 kGroup. (In one go, 296 parts of 8 rows at D = 256
             // took 90 us.)
-            const int start = s_before + seg * (units + kSegment) + kSegment;
-            const int c0 = s_plan.c0 >= 0 ? s_plan.c0 : s_plan.owner(start);
-            const int c1 = s_plan.c0 >= 0 ? s_plan.c1 : s_plan.owner(start + units - 1);
+            const int per = s_plan.shares.per, start = s_before + seg * (units + per) + per;
+            const int c0 = s_plan.c0 >= 0 ? s_plan.c0 : s_plan.shares.owner(start);
+            const int c1 = s_plan.c0 >= 0 ? s_plan.c1 : s_plan.shares.owner(start + units - 1);
             const int parts = c1 - c0 + 1;
             const bool two = parts > 3 * kGroup;
 #pragma unroll 1

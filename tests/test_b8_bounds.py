@@ -2,6 +2,7 @@
 the precision that include/tq.h states."""
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -35,7 +36,91 @@ def test_shuffles_name_their_threads():
         assert "__activemask" not in source(name), name
 
 
+SHARES = r"""
+#include <cstdio>
+#include "b8_shares.h"
+// units, segments and CTAs on each line of input: shares have to be in order, cover the price and know their own units
+int main() {
+    long long units, segments, ctas;
+    while (scanf("%lld %lld %lld", &units, &segments, &ctas) == 3) {
+        B8Shares s;
+        s.make((int)units, (int)segments, (int)ctas);
+        const long long price = units + (long long)s.per * segments;
+        bool good = s.per >= 0 && price < (1ll << 31) && s.price((int)units, (int)segments) == price && s.share(0) == 0 &&
+                    s.share((int)ctas) == price && s.base > 0;
+        for (int c = 0; good && c < ctas; ++c) {
+            const int lo = s.share(c), hi = s.share(c + 1);
+            good = lo < hi && s.owner(lo) == c && s.owner(hi - 1) == c;
+        }
+        printf("%d %d\n", (int)good, s.per);
+    }
+}
+"""
+
+
+def test_equal_shares_over_the_largest_lists(tmp_path):
+    """The host accepts (blocks + 1) x segments up to 2^30; a segment has at most two units more than blocks: up to 2^29
+    segments of one to three units. Their shares are worked out in 32 bits."""
+    (tmp_path / "shares.cpp").write_text(SHARES)
+    subprocess.check_call(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", CSRC, "-o",
+                           str(tmp_path / "shares"), str(tmp_path / "shares.cpp")])
+    cases = []
+    for segments in (1, 2, 295, 296, 297, 5000, 10 ** 6, 195225786, 195225787, 214954800, 196608000, 2 ** 28, 390451573, 2 ** 29 - 1, 2 ** 29):
+        for each in (1, 2, 3, 31, 33, 2 ** 10, 2 ** 23):
+            units = segments * each
+            if segments * max(2, each - 1) <= 2 ** 30:
+                cases += [(units, segments, c) for c in {1, 2, min(units, 7), min(units, 296), min(units, 384)} if c <= units]
+    r = subprocess.run([str(tmp_path / "shares")], input="\n".join("%d %d %d" % c for c in cases), text=True,
+                       capture_output=True, check=True)
+    out = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+    assert len(out) == len(cases) > 200
+    for case, (good, per) in zip(cases, out):
+        assert good, case
+        assert (per == 0) == (case[0] + 10 * case[1] >= 2 ** 31), case       # priced beside its units wherever that fits
+
+
 # ----------------------------------------------------------------------------- GPU
+@pytest.mark.gpu
+def test_selections_of_196_million_segments(m):
+    """An accepted call whose segments' prices together pass 31 bits: 4096 sequences x 6000 query tokens x 8 kv heads, one
+    block of 32 tokens each. Every row is written; those of every 64th sequence are compared."""
+    import torch
+    d, n_kv, n_seq, n_q, nb = 8, 8, 4096, 6000, 188
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    pages = torch.zeros(nb, m.tq_b8_page_bytes(d, n_kv), dtype=torch.uint8, device="cuda")
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").repeat(n_seq, 1)
+    length = torch.full((n_seq,), 32 * nb, dtype=torch.int32, device="cuda")
+    open_ = torch.zeros(n_seq, n_kv, 2, 32, d, dtype=torch.bfloat16, device="cuda")
+    ws = m.workspace(256)
+    one = m.Cache8(d, pages, table[:1], length[:1], open_[:1])                   # the pages that all sequences share
+    k, v = (torch.randn(1, 32 * nb, n_kv, d, generator=gen, device="cuda") for _ in range(2))
+    m.tq_b8_append(one, k, v, ws)
+    m.tq_b8_read(one, k, v, ws)                                                  # as the cache holds them
+    cache = m.Cache8(d, pages, table, length, open_)
+    q = torch.randn(n_seq, n_q, n_kv, d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    sel = torch.randint(0, nb, (n_seq, n_q, n_kv, 1), generator=gen, device="cuda", dtype=torch.int32)
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    ws = m.workspace(m.tq_b8_workspace_bytes(cache, n_q, 1, 1, weights=False))
+    m.tq_b8_attention(cache, q, d ** -0.5, out, ws, sel=sel)
+    assert m.tq_get_status(ws) == m.TQ_OK
+    assert not any(torch.isnan(out[s:s + 256]).any() for s in range(0, n_seq, 256))
+    kb, vb = (x[0].view(nb, 32, n_kv, d).permute(2, 0, 1, 3).double() for x in (k, v))  # [n_kv, nb, 32, d]
+    heads, t = torch.arange(n_kv, device="cuda"), torch.arange(32, device="cuda")
+    last = 32 * nb - n_q + torch.arange(n_q, device="cuda")
+    for s in list(range(0, n_seq, 64)) + [n_seq - 1]:
+        b = sel[s, :, :, 0].long()                                               # [n_q, n_kv]
+        kk, vv = kb[heads, b], vb[heads, b]                                      # [n_q, n_kv, 32, d]
+        seen = 32 * b[..., None] + t <= last[:, None, None]
+        l = torch.einsum("qhd,qhtd->qht", q[s].double(), kk) * d ** -0.5
+        top = torch.where(seen, l, -torch.inf).amax(-1, keepdim=True)
+        w = torch.where(seen, torch.exp(l - torch.where(top > -torch.inf, top, 0.0)), 0.0)
+        w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
+        want, size = torch.einsum("qht,qhtd->qhd", w, vv), torch.einsum("qht,qhtd->qhd", w, vv.abs())
+        # with |q| <= 6 and sum |k| <= 48 a logit is off by 8 ** -0.5 * 2^-22 * 6 * 48 for q's fixed point and as much for
+        # the fp32 factors, 5e-5 in all; weights move by twice that, their sums and the quotient by a few 2^-22: 2^-13
+        assert ((out[s].double() - want).abs() <= 2.0 ** -13 * size.amax(-1, keepdim=True)).all(), s
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,g,n_q", [(64, 4, 1), (40, 3, 1), (64, 4, 2), (64, 16, 1)])
 def test_attention_where_some_warps_have_nothing(m, d, g, n_q):
