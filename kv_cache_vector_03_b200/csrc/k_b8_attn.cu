@@ -2,7 +2,7 @@
 //
 // Mathematics. With key codes c_t (scale s), value codes v_t (scale u), l_t = s <q, c_t> scale log2(e) and a reference m,
 //   o = sum_t 2^(l_t - m) u v_t / sum_t 2^(l_t - m)
-// over 32-token blocks, m following the largest logit (online softmax; only when it is passed by 2^8, which changes
+// over 32-token blocks, m following the largest logit (online softmax; only when it is passed by 2^6, which changes
 // nothing but the exponents' range).
 //
 // Work is a list of units: a 32-token block, or 16 tokens of an open block, for one (sequence, kv head, tile of 8 or 16
@@ -21,9 +21,12 @@
 //     this costs 90.)
 //   O^T += V^T P^T in fp16: a byte permute into 1024 + (code + 128) and a subtraction of 1152 make exact fp16 codes. The
 //     weights are two fp16 pieces: one alone is off by 2^-12, which an fp32 result shows. Each block's sum is scaled by
-//     u into fp32 registers.
-// Key scale and softmax scale are one product kept in two floats, applied with one rounding next to m, so that a
-// logit of 30 loses no more than one of 1: results are off by 3e-7, an fp32 evaluation by 2e-6.
+//     u into fp32 registers. The pieces hold 22 bits of a weight down to 2^-12 of the one at m; below, they are off by
+//     2^-34 of that. So m goes by tokens that have a value: one whose value codes are all zeros (an attention sink) may pass it
+//     by 2^80 and counts in the denominator alone. (With m at a sink 20 nats above 8192 tokens, what these add up to was
+//     off by 7e-4 of itself, and lost from 23 nats on.)
+// Key scale and softmax scale are one product kept in two floats and applied next to m, so a logit is off by little more
+// than the rounding of its whole-number sum to fp32, 2^-24 of it.
 //
 // fp32 work goes two at a time (f2_*, rounded the same): 64 x 8192 181 -> 174 us.
 //
@@ -42,8 +45,9 @@
 namespace {
 
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr float kBias = 7.f;         // weights are kept as 2^(7 + logit - m): their small pieces stay normal in fp16
-constexpr float kSlack = 8.f;        // m follows the maximum once it is passed by 2^8: 2^(7 + 8) < 65504
+constexpr float kBias = 9.f;         // weights are kept as 2^(9 + logit - m),
+constexpr float kSlack = 6.f;        // m follows the maximum once it is passed by 2^6: 2^(9 + 6) < 65504
+constexpr float kSink = 80.f;        // tokens whose values are all zeros may pass m by 2^80
 // units a CTA takes at least, where segments are shared (one sequence of 8192 tokens: with 4 21.2 us, 8 18.6; 16 ragged ones
 // of 1500: with 8 20.5 us, 16 28.7)
 constexpr int kMinUnits = 8;
@@ -667,14 +671,42 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                         }
                     }
                 }
+                uint32_t zeros = 0;                           // which tokens' values are all zeros, where it matters
                 if (__any_sync(0xffffffffu, grown)) {
+                    if (what >= 0) {
+                        // token `lane`: channels 0 .. 3, which seldom are zeros all, before the rest
+                        const uint8_t* row = vp + lane * D;
+                        const uint32_t four = *reinterpret_cast<const uint32_t*>(row + (b8_swz(lane, D / 16) << 4));
+                        zeros = __ballot_sync(0xffffffffu, four == 0x80808080u);
+                        if (zeros) {
+                            bool none = four == 0x80808080u;
+#pragma unroll 1
+                            for (int k = 0; none && k < D / 16; ++k) {
+                                const uint4 a = *reinterpret_cast<const uint4*>(row + ((k ^ (lane & (D / 16 - 1))) << 4));
+                                none = (a.x & a.y & a.z & a.w) == 0x80808080u && (a.x | a.y | a.z | a.w) == 0x80808080u;
+                            }
+                            zeros = __ballot_sync(0xffffffffu, none);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    top[nt][e] = -INFINITY;
+#pragma unroll
+                                    for (int t = 0; t < 4; ++t) {
+                                        const float y = __fmul_rn(sc[t >> 1][nt][2 * (t & 1) + e], e ? ga[nt].y : ga[nt].x);
+                                        if (!(masked && gone(nt, e, t))) top[nt][e] = fmaxf(top[nt][e], zeros >> (gq + 8 * t) & 1u ? y - kSink : y);
+                                    }
+                                }
+                        }
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float t = fmaxf(m[nt][e], top[nt][e]);
+                            float t = top[nt][e];
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                            t = fmaxf(m[nt][e], ceilf(t));        // whole numbers: no difference of two of them is rounded
                             const float f = m[nt][e] == -INFINITY ? 0.f : tq_exp2(m[nt][e] - t);
                             m[nt][e] = t;
                             big = big || (fabsf(t) >= 65536.f && t != -INFINITY);
@@ -708,7 +740,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             float* x = &sc[t >> 1][nt][2 * (t & 1)];
-                            const float2 v2 = make_float2(x[0], x[1]), y = f2_fma(v2, ga[nt], f2_fma(v2, gb[nt], ref));
+                            const float2 v2 = make_float2(x[0], x[1]), y = f2_fma(v2, gb[nt], f2_fma(v2, ga[nt], ref));
                             x[0] = y.x;
                             x[1] = y.y;
                         }
@@ -734,6 +766,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                         l[nt][0] = y.x;
                         l[nt][1] = y.y;
                     }
+                if (zeros) {                                  // their weights may pass fp16, and have nothing to weigh
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (zeros >> (gq + 8 * t) & 1u) sc[t >> 1][nt][2 * (t & 1)] = sc[t >> 1][nt][2 * (t & 1) + 1] = 0.f;
+                }
                 if (what >= 0) {
                     uint32_t pf[2][NT][2][2];                 // P^T as B fragments: [token half][n-tile][piece][register]
 #pragma unroll

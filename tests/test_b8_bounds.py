@@ -139,3 +139,84 @@ def test_attention_where_some_warps_have_nothing(m, d, g, n_q):
             want, _, size, reach = ref.attention(sq, q64[s], scale)
             close(got[s], want, size, reach, d)
     assert p.ok(ws)
+
+
+def fill(p, k, v):
+    """k, v [n_seq, n, n_kv, d] (numpy) into an empty Pair."""
+    p.length += k.shape[1]
+    m, cuda = p.m, lambda x: p.torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda()
+    m.tq_b8_append(p.cache, cuda(k), cuda(v), p.ws)
+    for s, sq in enumerate(p.seqs):
+        sq.append(k[s], v[s])
+
+
+def within(got, sq, q, scale, lost=0.0, n_sum=64):
+    """Output rows against 64 bits, where a logit of whole pages is off by 2^-23 of itself (its whole-number sum and its
+    distance to the block's largest in fp32), by 2^-24 max |q| max |k| (the small pieces' share of that sum) and by
+    `lost`, what q itself loses. Weights move by twice that; their pieces, exponentials, matrix products and up to n_sum
+    additions in a row are off by 2^-24 of sum w |v| each (n_sum + 64 of them in all)."""
+    want, weight, size, _ = ref.attention(sq, q, scale)
+    k = np.abs(sq.values()[:, :, 0])                                             # [n, n_kv, d]
+    logit = np.abs(scale * np.einsum("ihgd,nhd->ihgn", q, sq.values()[:, :, 0])).max(axis=-1)
+    dl = 2.0 ** -23 * logit + abs(scale) * 2.0 ** -24 * np.abs(q).max(axis=-1) * k.max() + lost
+    bound = (np.expm1(2 * dl) + (n_sum + 64) * 2.0 ** -24) * size
+    err = np.abs(got - want).max(axis=-1)
+    assert np.isfinite(got).all()
+    assert (err <= bound + 1e-30).all(), (float((err / np.maximum(bound, 1e-30)).max()), (err / np.maximum(size, 1e-300)).max(axis=(0, 1, 2)))
+    return dl
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g,n,where,heavy", [
+    (128, 4, 64, 0, 0.0), (128, 4, 2048, 5, 0.0), (64, 3, 64, 31, 2e-3), (64, 3, 2048, 1000, 0.0), (256, 2, 1024, 3, 0.0),
+    (128, 16, 2048, 0, 2e-3), (64, 16, 64, 7, 0.0), (128, 4, 64, 0, 0.02), (80, 4, 96, 40, 0.0), (8, 2, 64, 9, 0.0),
+    (128, 4, 64, 0, 1.0)])
+def test_attention_sinks(m, d, g, n, where, heavy):
+    """One token lies 8 to 60 nats above the rest, and its value is zero, rounds to zero, is small or as large as the others':
+    what the light tokens add keeps its precision, in the heavy token's block and in others."""
+    gaps = [8.0, 12.0, 16.0, 20.0, 22.0, 27.0, 35.0, 60.0]
+    n_kv, scale = 2, d ** -0.5
+    p = Pair(m, d, n_kv, len(gaps), n // 32 + 1, 90 + d + g + n, width=32768 // n_kv if g > 8 else None)
+    k = p.rng.standard_normal((len(gaps), n, n_kv, d))
+    v = p.rng.standard_normal((len(gaps), n, n_kv, d))
+    k[..., 0] = 0.0
+    k[:, where], v[:, where] = 0.0, v[:, where] * heavy
+    k[:, where, :, 0] = (np.array(gaps) / (4.0 * scale))[:, None]
+    fill(p, k, v)
+    q = np.rint(64 * p.rng.standard_normal((len(gaps), 1, n_kv, g, d)).clip(-3.9, 3.9)) / 64    # exact in 22 bits
+    q[..., 0] = 4.0
+    qt = p.torch.from_numpy(q.astype(np.float32).reshape(len(gaps), 1, n_kv * g, d)).cuda()
+    ws = p.workspace(1, g)
+    out = p.torch.full(qt.shape, float("nan"), device="cuda")
+    m.tq_b8_attention(p.cache, qt, scale, out, ws)
+    acc = p.torch.zeros(len(gaps), n_kv, 32 * p.nb, device="cuda")
+    again = p.torch.full(qt.shape, float("nan"), device="cuda")
+    m.tq_b8_attention(p.cache, qt, scale, again, ws, acc_out=acc)
+    assert p.torch.equal(out, again) and p.ok(ws)
+    got = out.double().cpu().numpy().reshape(q.shape)
+    for s, sq in enumerate(p.seqs):
+        within(got[s], sq, q[s], scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g,n_q", [(128, 4, 1), (64, 2, 3), (40, 9, 1)])
+def test_attention_over_values_of_zeros(m, d, g, n_q):
+    """Blocks and tokens whose values are all zeros, or zeros in the first channels alone, count in the weights."""
+    n, n_kv, scale = 192, 2, d ** -0.5
+    p = Pair(m, d, n_kv, 2, 7, 95 + d)
+    k, v = p.rng.standard_normal((2, n, n_kv, d)), p.rng.standard_normal((2, n, n_kv, d))
+    v[:, :32] = 0.0
+    v[:, 32:64, 0] = 0.0
+    v[:, 40:70] = 0.0
+    v[:, 96:120, :, :8] = 0.0
+    v[1, 128:191] = 0.0                                                          # all but the last token of two blocks
+    fill(p, k, v)
+    q = np.rint(64 * p.rng.standard_normal((2, n_q, n_kv, g, d))) / 64
+    qt = p.torch.from_numpy(q.astype(np.float32).reshape(2, n_q, n_kv * g, d)).cuda()
+    ws = p.workspace(n_q, g)
+    out = p.torch.full(qt.shape, float("nan"), device="cuda")
+    m.tq_b8_attention(p.cache, qt, scale, out, ws)
+    got = out.double().cpu().numpy().reshape(q.shape)
+    for s, sq in enumerate(p.seqs):
+        within(got[s], sq, q[s], scale)
+    assert p.ok(ws)
