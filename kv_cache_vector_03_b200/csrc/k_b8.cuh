@@ -105,9 +105,10 @@ struct B8AttnParams {
     float* acc_out;
     float decay;
     float* out;
-    float* logits;           // [n_seq * n_kv][n_q * g][logit_row] log2-domain logits, when acc_out is asked for
-    float* lse;              // [n_seq * n_kv][n_q * g]
-    int64_t logit_row;
+    float* logits;           // [n_seq * n_kv][n_q * g][logit_row], when acc_out is asked for: a row's tokens, their logits in the
+                             // log2 domain next to the reference of their unit (k_b8_attn.cu), and from ref_at on these references
+    float2* norm;            // [n_seq * n_kv][n_q * g] a row's reference and what its weights are multiplied with
+    int64_t logit_row, ref_at;
     float* part;             // [2 grid][row_tile][D] partial value sums, [2 grid][row_tile][2] their maximum and sum
     float* part_ml;
     uint32_t* count;         // kB8Counters bytes, zero between calls: how many parts of a segment have arrived

@@ -56,7 +56,7 @@ constexpr int kMinUnits = 8;
 constexpr int kWholeUnits = 32;
 constexpr int kStraddle = 24;        // price of a cut inside a CTA's share, in units (10000 cycles)
 constexpr int kGroup = 16;           // parts that are joined at a time, where there are many
-constexpr int kAccTok = 128;        // threads of a CTA that adds up weights (256 with 2 tokens each: 1 us more for 16 x 8100)
+constexpr int kAccTok = 128;        // threads of a CTA that adds up weights
 
 // Two CTAs share an SM, so that one computes while the other starts or joins a segment (one CTA of 16 warps: 205 us for
 // 64 x 8192; two of 8: 199). Warps and ring stages of one of them, and in how many rounds its warps' sums meet in shared
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             for (int hr = w; hr < c.n_kv * rows; hr += NW) {
                 float* out = p.out + q_row(v, hr / rows, hr % rows) * c.d;
                 for (int e = lane; e < c.d; e += 32) out[e] = 0.f;
-                if (WT && lane == 0) p.lse[(int64_t)v * c.n_kv * rows + hr] = INFINITY;
+                if (WT && lane == 0) p.norm[(int64_t)v * c.n_kv * rows + hr] = make_float2(0.f, 0.f);
             }
         }
     }
@@ -541,9 +541,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             // where in a row of logits this unit's are
             const int at = off + i - u, pages = SP ? p.n_sel : n >> 5, col = at < pages ? 32 * at : 32 * pages + 16 * (at - pages);
             // (an open half is 16 tokens, and nothing only where a wait has run out)
-            if (WT && what == -1 && (at < pages || lane < 16))
-                for (int r = 0; r < 8 * NT && row0 + r < rows; ++r)
-                    p.logits[(((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0 + r) * p.logit_row + col + lane] = -INFINITY;
+            if (WT && what == -1)
+                for (int r = 0; r < 8 * NT && row0 + r < rows; ++r) {
+                    float* to = p.logits + (((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0 + r) * p.logit_row;
+                    if (at < pages || lane < 16) to[col + lane] = -INFINITY;
+                    if (lane == 0) to[p.ref_at + at] = 0.f;
+                }
             if (what != -1) {
                 float sc[2][NT][4];                           // S^T: tokens 16 mt + gq (+ 8), rows 2 tq, 2 tq + 1
                 const uint8_t* kp = smem + (size_t)st * SB;
@@ -654,23 +657,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     top[nt][1] = fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y));
                     grown = grown || top[nt][0] > m[nt][0] + kSlack || top[nt][1] > m[nt][1] + kSlack;
                 }
-                if (WT) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float* to = lg + col + 8 * nt * p.logit_row;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const float2 raw = make_float2(sc[t >> 1][nt][2 * (t & 1)], sc[t >> 1][nt][2 * (t & 1) + 1]);
-                            float2 y = f2_fma(raw, ga[nt], f2_mul(raw, gb[nt]));
-                            if (masked && gone(nt, 0, t)) y.x = -INFINITY;
-                            if (masked && gone(nt, 1, t)) y.y = -INFINITY;
-                            if (what >= 0 || t < 2) {                            // (an open half is 16 tokens)
-                                if (row0 + 8 * nt + 2 * tq < rows) to[8 * t] = y.x;
-                                if (row0 + 8 * nt + 2 * tq + 1 < rows) to[p.logit_row + 8 * t] = y.y;
-                            }
-                        }
-                    }
-                }
                 uint32_t zeros = 0;                           // which tokens' values are all zeros, where it matters
                 if (__any_sync(0xffffffffu, grown)) {
                     if (what >= 0) {
@@ -754,6 +740,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
 #pragma unroll
                             for (int t = 0; t < 4; ++t)
                                 if (gone(nt, e, t)) sc[t >> 1][nt][2 * (t & 1) + e] = -INFINITY;
+                }
+                if (WT) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* to = lg + col + 8 * nt * p.logit_row;
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (what >= 0 || t < 2) {                            // (an open half is 16 tokens)
+                                if (row0 + 8 * nt + 2 * tq < rows) to[8 * t] = sc[t >> 1][nt][2 * (t & 1)];
+                                if (row0 + 8 * nt + 2 * tq + 1 < rows) to[p.logit_row + 8 * t] = sc[t >> 1][nt][2 * (t & 1) + 1];
+                            }
+                        to += p.ref_at + at - col;
+                        if (gq == 0 && row0 + 8 * nt + 2 * tq < rows) to[0] = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+                        if (gq == 0 && row0 + 8 * nt + 2 * tq + 1 < rows) to[p.logit_row] = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                    }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -993,13 +994,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                 }
             }
         }
-        float* lse = p.lse + ((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0;
+        float2* norm = p.norm + ((int64_t)s * c.n_kv + h) * (p.n_q * p.g) + row0;
+        // (logits below m hold kBias too, and so does the sum)
+        auto norm_of = [](float top, float sum) {
+            return sum == 0.f ? make_float2(0.f, 0.f) : make_float2(top == -INFINITY ? 0.f : top, 1.f / sum);
+        };
         if (threadIdx.x < 8 * NT && row0 + threadIdx.x < rows) {
             const float top = s_top[threadIdx.x], sum = s_sum[threadIdx.x];
             if (!whole)
                 *reinterpret_cast<float2*>(p.part_ml + (slot * 8 * NT + threadIdx.x) * 2) = make_float2(top, sum);
             else if (WT)
-                lse[threadIdx.x] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+                norm[threadIdx.x] = norm_of(top, sum);
         }
         __syncthreads();                                  // s_o and the row sums are free again
         if (!whole) {
@@ -1070,7 +1075,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     if (lane == 0) {
                         s_top[r] = top;
                         s_sum[r] = sum;
-                        if (WT && done) lse[r] = sum == 0.f ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - kBias;
+                        if (WT && done) norm[r] = norm_of(top, sum);
                     }
                 }
                 __syncthreads();
@@ -1139,18 +1144,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
     }
 }
 
-// acc_out[t] = decay * acc_in[t] + sum over rows of 2^(logit - lse), rows in order: one thread adds up a token, so
-// nothing is added atomically. A thread has kAccPer tokens and takes four rows at a time, to have that many loads under
-// way. With a selection a table in shared memory says which of its entries holds a block.
+// acc_out[t] = decay * acc_in[t] + sum over rows of 2^(x + (ref - top)) / sum, rows in order, with a token's logit x next to
+// its unit's reference ref and the row's reference top: whole numbers, so a weight is as precise as in the value sum,
+// however large the logits are. One thread adds up a token, so nothing is added atomically. A thread has kAccPer tokens next
+// to each other, which share a reference, and takes four rows at a time, to have that many loads under way (registers for
+// them at 8 CTAs an SM; left to itself the compiler takes 32 and waits: one sequence of 4000 tokens 19.9 us instead of 18.0).
+// With a selection a table in shared memory says which of its entries holds a block.
 constexpr int kAccPer = 4, kAccTile = kAccTok * kAccPer;
-__global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8AttnParams p, int splits) {
+__global__ void __launch_bounds__(kAccTok, 8) k_b8_acc(const __grid_constant__ B8AttnParams p, int splits) {
     const B8Cache& c = p.c;
     tq_pdl_launch_dependents();
     tq_pdl_wait();
     const int sh = blockIdx.x / splits, s = sh / c.n_kv;
     const int n = b8_len(c, s), nfull = n >> 5, rows = p.n_q * p.g;
-    const float* lse = p.lse + (int64_t)sh * rows;
+    const float2* norm = p.norm + (int64_t)sh * rows;
     const int64_t at = (int64_t)sh * c.max_blocks * 32;
+    const bool wide = (((uintptr_t)p.acc_in | (uintptr_t)p.acc_out) & 15) == 0;   // (rows are multiples of 128 bytes)
     __shared__ int s_at[kAccTile / 32];
     for (int t0 = (blockIdx.x - sh * splits) * kAccTile; t0 < n; t0 += splits * kAccTile) {
         if (p.sel) {
@@ -1163,34 +1172,56 @@ __global__ void __launch_bounds__(kAccTok) k_b8_acc(const __grid_constant__ B8At
             }
             __syncthreads();
         }
-        float a[kAccPer], w[kAccPer];
-        const float* lg[kAccPer];
+        const int i = kAccPer * threadIdx.x, t = t0 + i;
+        if (t >= n) continue;
+        const bool all = wide && t + kAccPer <= n - p.n_q;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.acc_in && all) {
+            a = *reinterpret_cast<const float4*>(p.acc_in + at + t);
+            a = make_float4(p.decay * a.x, p.decay * a.y, p.decay * a.z, p.decay * a.w);
+        } else if (p.acc_in) {
+            float* to = &a.x;
 #pragma unroll
-        for (int k = 0; k < kAccPer; ++k) {
-            const int i = threadIdx.x + k * kAccTok, t = t0 + i;
-            a[k] = p.acc_in && t < n - p.n_q ? p.decay * p.acc_in[at + t] : 0.f;
-            const int u = t >= n ? -1 : p.sel ? s_at[i >> 5] : t >> 5;
-            lg[k] = u < 0 ? nullptr : p.logits + (int64_t)sh * rows * p.logit_row + (int64_t)u * 32 + (t & 31);
-            w[k] = 0.f;
+            for (int k = 0; k < kAccPer; ++k)
+                if (t + k < n - p.n_q) to[k] = p.decay * p.acc_in[at + t + k];
         }
-        for (int r0 = 0; r0 < rows; r0 += 4) {
-            float e[4], y[kAccPer][4];
+        const int u = p.sel ? s_at[i >> 5] : t >> 5;         // where the tokens are in a row of logits
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u >= 0) {
+            const bool half = u == (p.sel ? p.n_sel : nfull) && (t & 16);            // the open block's second
+            const float* lg = p.logits + (int64_t)sh * rows * p.logit_row;
+            const int64_t col = (int64_t)u * 32 + (t & 31), ref = p.ref_at + u + (half ? 1 : 0);
+            for (int r0 = 0; r0 < rows; r0 += 4) {
+                float2 e[4];
+                float4 y[4];
+                float d[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                e[r] = r0 + r < rows ? lse[r0 + r] : INFINITY;
+                for (int r = 0; r < 4; ++r) {
+                    const int rr = min(r0 + r, rows - 1);            // (a row behind the last counts 0)
+                    const float* row = lg + rr * p.logit_row;
+                    e[r] = norm[rr];
+                    y[r] = *reinterpret_cast<const float4*>(row + col);
+                    d[r] = row[ref];
+                    if (r0 + r >= rows) e[r].y = 0.f;
+                }
 #pragma unroll
-                for (int k = 0; k < kAccPer; ++k) y[k][r] = lg[k] && r0 + r < rows ? lg[k][(r0 + r) * p.logit_row] : 0.f;
+                for (int r = 0; r < 4; ++r) {
+                    const float down = d[r] - e[r].x;
+                    w.x = fmaf(tq_exp2(y[r].x + down), e[r].y, w.x);
+                    w.y = fmaf(tq_exp2(y[r].y + down), e[r].y, w.y);
+                    w.z = fmaf(tq_exp2(y[r].z + down), e[r].y, w.z);
+                    w.w = fmaf(tq_exp2(y[r].w + down), e[r].y, w.w);
+                }
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int k = 0; k < kAccPer; ++k)
-                    if (lg[k] && e[r] != INFINITY) w[k] += tq_exp2(y[k][r] - e[r]);
         }
+        w = make_float4(a.x + w.x, a.y + w.y, a.z + w.z, a.w + w.w);
+        if (wide && t + kAccPer <= n) {
+            *reinterpret_cast<float4*>(p.acc_out + at + t) = w;
+        } else {
+            const float v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int k = 0; k < kAccPer; ++k) {
-            const int t = t0 + threadIdx.x + k * kAccTok;
-            if (t < n) p.acc_out[at + t] = a[k] + w[k];
+            for (int k = 0; k < kAccPer; ++k)
+                if (t + k < n) p.acc_out[at + t + k] = v[k];
         }
     }
 }

@@ -60,14 +60,15 @@ B8Cache view(const tq_b8_cache* c, void* ws) {
 }
 
 // regions after the status word; a call uses those of its own kind, so they share the space
-struct B8Ws { size_t key, part, ml, lse, logits, total; int64_t logit_row; int rows, row_tile; };
+struct B8Ws { size_t key, part, ml, norm, logits, total; int64_t logit_row, ref_at; int rows, row_tile; };
 B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     B8Ws w = {};
     const size_t rows = (size_t)c->n_seq * c->n_kv * (size_t)n_q;
     size_t off = TQ_STATUS_BYTES;
     w.key = off;
     const size_t select_end = align_up(off + (n_sel ? rows * (size_t)c->max_blocks * 4 : 0));
-    w.logit_row = n_sel ? (int64_t)(n_sel + 1) * kB8Block : c->max_blocks * kB8Block;
+    w.ref_at = n_sel ? (int64_t)(n_sel + 1) * kB8Block : c->max_blocks * kB8Block;   // then a reference per unit: the halves of an
+    w.logit_row = w.ref_at + (w.ref_at / kB8Block + 1 + 31) / 32 * 32;              // open block are two
     // rows and blocks of one virtual sequence (k_b8_attn.cu): of a sequence, with a selection of a query token
     w.rows = n_sel ? g : n_q * g;
     const int64_t blocks = c->n_seq * c->n_kv * (n_sel ? (int64_t)n_q * n_sel : c->max_blocks);
@@ -75,7 +76,7 @@ B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     const size_t slots = rows && g ? 2 * (size_t)b8_attn_grid() * tile : 0;
     w.part = off; off = align_up(off + slots * b8_padded(c->d) * 4);
     w.ml = off; off = align_up(off + slots * 8);
-    w.lse = off; off = align_up(off + (weights ? rows * g * 4 : 0));
+    w.norm = off; off = align_up(off + (weights ? rows * g * 8 : 0));
     w.logits = off; off = align_up(off + (weights ? rows * g * (size_t)w.logit_row * 4 : 0));
     w.total = std::max(select_end, off);
     return w;
@@ -161,9 +162,9 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     p.sel = sel; p.n_sel = n_sel;
     p.acc_in = acc_in; p.acc_out = acc_out; p.decay = decay;
     p.out = out;
-    p.lse = reinterpret_cast<float*>(wsb + W.lse);
+    p.norm = reinterpret_cast<float2*>(wsb + W.norm);
     p.logits = reinterpret_cast<float*>(wsb + W.logits);
-    p.logit_row = W.logit_row;
+    p.logit_row = W.logit_row; p.ref_at = W.ref_at;
     p.part = reinterpret_cast<float*>(wsb + W.part);
     p.part_ml = reinterpret_cast<float*>(wsb + W.ml);
     p.count = reinterpret_cast<uint32_t*>(wsb) + 16;

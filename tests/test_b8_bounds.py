@@ -220,3 +220,64 @@ def test_attention_over_values_of_zeros(m, d, g, n_q):
     for s, sq in enumerate(p.seqs):
         within(got[s], sq, q[s], scale)
     assert p.ok(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,selected", [(60, False), (64, False), (47, True), (33, True)])
+def test_accumulated_weights_of_large_logits(m, n, selected):
+    """A row's accumulated weights are those of its value sum and add up to 1, however large the logits are. Keys and
+    queries are whole numbers, keys with an element of 127 (scale 1) and each there several times, values the unit vectors:
+    equal logits are equal in every path, the output is the weights themselves."""
+    import torch
+    d, n_kv, g = 64, 2, 3
+    for scale in (1e-5, 1e-4, 1e-3, 0.01, 0.1, 1.0, 10.0, 1e2, 1e4, -1e-3, -1.0, -1e4):
+        p = Pair(m, d, n_kv, 1, 3, 110)
+        kinds = np.rint(60 * p.rng.standard_normal((8, n_kv, d))).clip(-126, 126)
+        kinds[..., 0] = 127
+        k, v = kinds[np.arange(n) % 8][None], np.zeros((1, n, n_kv, d))
+        v[0, np.arange(n), :, np.arange(n)] = 1.0
+        fill(p, k, v)
+        q = np.rint(50 * p.rng.standard_normal((1, 1, n_kv, g, d)))
+        qt = torch.from_numpy(q.astype(np.float32).reshape(1, 1, n_kv * g, d)).cuda()
+        want, weight, _, _ = ref.attention(p.seqs[0], q[0], scale)
+        sel = torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda").expand(1, 1, n_kv, 3).contiguous() if selected else None
+        ws = p.workspace(1, g, 3 if selected else 0)
+        out, acc = torch.zeros(qt.shape, device="cuda"), torch.zeros(1, n_kv, 32 * p.nb, device="cuda")
+        m.tq_b8_attention(p.cache, qt, scale, out, ws, sel=sel, acc_out=acc)
+        assert p.ok(ws)
+        w = out.double().cpu().numpy().reshape(n_kv, g, d)[..., :n]                   # a weight per token
+        a = acc[0].double().cpu().numpy()[:, :n]
+        # two ways to the same weights: pieces of 22 bits (off by 2^-34 at least) and fp32 sums against fp32 sums
+        assert (np.abs(a - w.sum(axis=1)) <= 2.0 ** -18 * a + g * 2.0 ** -33).all(), scale
+        assert (np.abs(a.sum(axis=1) - g) <= g * 2.0 ** -18).all(), (scale, a.sum(axis=1))
+        # against 64 bits: a logit is off by 2^-22 of itself (ties stay ties); where rows are ties of whole numbers apart, by nothing
+        logits = np.abs(scale) * np.abs(np.einsum("hgd,nhd->hgn", q[0, 0], p.seqs[0].values()[:, :, 0])).max(axis=(1, 2))
+        rel = np.expm1(2 * np.minimum(logits * 2.0 ** -22, 1.0)) + 2.0 ** -18
+        if (logits * 2.0 ** -22 < 2.0 ** -6).all():
+            assert (np.abs(a - weight) <= rel[:, None] * weight + 2.0 ** -40).all(), scale
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_q,g,selected", [(1, 5, False), (3, 2, False), (1, 4, True)])
+def test_accumulated_weights_at_any_alignment(m, n_q, g, selected):
+    """acc_in and acc_out need be aligned to an element alone: the same bits as from 16-byte aligned ones."""
+    import torch
+    d, n_kv, lens = 64, 2, [0, 1, 30, 97, 160]
+    p = Pair(m, d, n_kv, len(lens), 6, 120)
+    p.append(lens)
+    q, _ = p.queries(n_q, g, "bf16")
+    sel = torch.tensor([0, 2, 3, -1], dtype=torch.int32, device="cuda").expand(len(lens), n_q, n_kv, 4).contiguous() if selected else None
+    ws = p.workspace(n_q, g, 4 if selected else 0)
+    shape, got = (len(lens), n_kv, 32 * p.nb), []
+    size = shape[0] * shape[1] * shape[2]
+    base = torch.rand(size, device="cuda")
+    for at_in, at_out in ((0, 0), (1, 0), (0, 3), (2, 1)):
+        room_in, room_out = torch.zeros(size + 4, device="cuda"), torch.full((size + 4,), 7.0, device="cuda")
+        a, b = room_in[at_in:at_in + size].view(shape), room_out[at_out:at_out + size].view(shape)
+        a.copy_(base.view(shape))
+        m.tq_b8_attention(p.cache, q, 0.1, torch.zeros(q.shape, device="cuda"), ws, sel=sel, acc_in=a, acc_out=b, decay=0.5)
+        got.append(b.clone())
+        assert (room_out[:at_out] == 7.0).all() and (room_out[at_out + size:] == 7.0).all()
+        for s, n in enumerate(lens):
+            assert (b[s, :, n:] == 7.0).all() and (b[s, :, :n] != 7.0).all()
+    assert all(torch.equal(got[0], x) for x in got[1:]) and p.ok(ws)
