@@ -385,10 +385,12 @@ int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dty
  *             n_q = 1 (else TQ_ERR_UNSUPPORTED) and no block may be named twice.
  *   out       device fp32 [n_seq, n_q, n_kv * g, d], 16-byte aligned.
  *   ws        tq_b8_workspace_bytes(cache, n_q, g, n_sel, acc_out != NULL) bytes.
- * Logits are exact products of the codes with q held to 22 bits (bf16 q: exactly). Weights
- * carry 22 bits into the value sum down to 2^-12 of the largest of them whose token has a value
- * (a code that is not 0), and are off by 2^-34 of that below; all sums are fp32. Runs give the
- * same bits every time. */
+ * q is held in fixed point, 22 bits below a row's largest element (bf16 elements down to 2^-14 of
+ * that exactly); its products with the codes are exact. A logit is off by at most
+ * scale 2^-22 max |q| sum |k| for that, and by 2^-23 of itself (tokens of the open block: by the
+ * fp32 sum of their products). Weights carry 22 bits into the value sum down to 2^-12 of the
+ * largest of them whose token has a value (a code that is not 0), and are off by 2^-34 of that
+ * below; all sums are fp32. Runs give the same bits every time. */
 int tq_b8_attention(const tq_b8_cache* cache, const void* q, tq_dtype q_dtype, int n_q, int g, float scale,
                     const int32_t* sel, int n_sel, const float* acc_in, float* acc_out, float decay, float* out,
                     void* ws, size_t ws_bytes, void* stream);

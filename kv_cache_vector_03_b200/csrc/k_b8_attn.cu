@@ -18,7 +18,8 @@
 //   S^T = K Q^T in int8: the stored bytes are unsigned, code + 128; q is scaled by a power of two per row to 22 bits and
 //     split into three int8 pieces; sums are exact in int32, start at -128 sum(q piece), and become floats through the
 //     bits of 1.5 * 2^23. No key is converted. (fp16 products of converted keys cost 170 instructions a unit where
-//     this costs 90.)
+//     this costs 90.) 22 bits below a row's largest element hold bf16 exactly down to 2^-14 of it; what is cut off moves a
+//     logit by up to scale 2^-22 max |q| sum |k|.
 //   O^T += V^T P^T in fp16: a byte permute into 1024 + (code + 128) and a subtraction of 1152 make exact fp16 codes. The
 //     weights are two fp16 pieces: one alone is off by 2^-12, which an fp32 result shows. Each block's sum is scaled by
 //     u into fp32 registers. The pieces hold 22 bits of a weight down to 2^-12 of the one at m; below, they are off by
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
             for (int k = 0; k < early; ++k) issue(w + NW * k, w + NW * k);
         }
         // q, while the first pages are on their way: a warp per row, a lane per 4 channels. A row is scaled by a
-        // power of two to below 2^22 and rounded to a whole number, which three int8 pieces hold.
+        // power of two to between 2^21 and 2^22 and rounded to whole numbers, which three int8 pieces hold.
 #pragma unroll 1
         for (int r = w; r < 8 * NT; r += NW) {
             constexpr int Q4 = D == 256 ? 2 : 1;

@@ -281,3 +281,32 @@ def test_accumulated_weights_at_any_alignment(m, n_q, g, selected):
         for s, n in enumerate(lens):
             assert (b[s, :, n:] == 7.0).all() and (b[s, :, :n] != 7.0).all()
     assert all(torch.equal(got[0], x) for x in got[1:]) and p.ok(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g,dtype", [(128, 4, "f32"), (128, 8, "bf16"), (64, 3, "f32"), (256, 2, "bf16"), (40, 5, "f32")])
+def test_attention_queries_of_a_wide_range(m, d, g, dtype):
+    """Elements of a row from 2^-24 to 1 of the largest, which meets keys of zero in half of the rows: a logit is off by at
+    most what q's fixed point loses, scale 2^-22 max |q| sum |k|. Rows whose elements fixed point holds are not off at all."""
+    import torch
+    n_kv, n, scale = 2, 160, d ** -0.5
+    p = Pair(m, d, n_kv, 2, 6, 130 + d + g)
+    k, v = p.rng.standard_normal((2, n, n_kv, d)), p.rng.standard_normal((2, n, n_kv, d))
+    k[0, ..., 0] = 0.0
+    fill(p, k, v)
+    q = np.exp2(p.rng.uniform(-20, 4, (2, 1, n_kv, g, d))) * p.rng.choice([-1.0, 1.0], (2, 1, n_kv, g, d))
+    q[..., 0] = 16 * (1 + 2.0 ** -7)
+    q[:, :, :, 0] = np.ldexp(np.rint(q[:, :, :, 0] * 2 ** 16), -16)              # 21 bits below 16: held
+    qt = torch.from_numpy(q.astype(np.float32).reshape(2, 1, n_kv * g, d)).cuda()
+    qt = qt if dtype == "f32" else qt.to(torch.bfloat16)
+    q = qt.double().cpu().numpy().reshape(q.shape)
+    ws = p.workspace(1, g)
+    out = torch.zeros(qt.shape, device="cuda")
+    m.tq_b8_attention(p.cache, qt, scale, out, ws)
+    got = out.double().cpu().numpy().reshape(q.shape)
+    for s, sq in enumerate(p.seqs):
+        reach = np.abs(sq.values()[:, :, 0]).sum(axis=2).max(axis=0)             # [n_kv]
+        lost = scale * 2.0 ** -22 * np.abs(q[s]).max(axis=-1) * reach[None, :, None]
+        within(got[s], sq, q[s], scale, lost=lost)
+        within(got[s][:, :, :1], sq, q[s][:, :, :1], scale)
+    assert p.ok(ws)
