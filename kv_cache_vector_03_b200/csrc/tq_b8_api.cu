@@ -59,13 +59,16 @@ B8Cache view(const tq_b8_cache* c, void* ws) {
     return v;
 }
 
-// regions after the status word; a call uses those of its own kind, so they share the space
+// regions after the status word; a call uses those of its own kind, so they share the space. total is 0 where the two that
+// grow with rows x blocks pass kMaxWs (the products of all limits pass 64 bits)
+constexpr size_t kMaxWs = (size_t)1 << 62;
 struct B8Ws { size_t key, part, ml, norm, logits, total; int64_t logit_row, ref_at; int rows, row_tile; };
 B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     B8Ws w = {};
     const size_t rows = (size_t)c->n_seq * c->n_kv * (size_t)n_q;
     size_t off = TQ_STATUS_BYTES;
     w.key = off;
+    if (n_sel && rows > kMaxWs / 4 / (size_t)c->max_blocks) return w;
     const size_t select_end = align_up(off + (n_sel ? rows * (size_t)c->max_blocks * 4 : 0));
     w.ref_at = n_sel ? (int64_t)(n_sel + 1) * kB8Block : c->max_blocks * kB8Block;   // then a reference per unit: the halves of an
     w.logit_row = w.ref_at + (w.ref_at / kB8Block + 1 + 31) / 32 * 32;              // open block are two
@@ -77,12 +80,14 @@ B8Ws b8_ws(const tq_b8_cache* c, int n_q, int g, int n_sel, bool weights) {
     w.part = off; off = align_up(off + slots * b8_padded(c->d) * 4);
     w.ml = off; off = align_up(off + slots * 8);
     w.norm = off; off = align_up(off + (weights ? rows * g * 8 : 0));
+    if (weights && rows * g > kMaxWs / 4 / (size_t)w.logit_row) return w;
     w.logits = off; off = align_up(off + (weights ? rows * g * (size_t)w.logit_row * 4 : 0));
     w.total = std::max(select_end, off);
     return w;
 }
 
 int check_ws(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return TQ_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256)) return TQ_ERR_ARG;
     return bytes < need ? TQ_ERR_WORKSPACE : TQ_OK;
 }

@@ -1,5 +1,6 @@
 """Paged 8-bit cache at its limits: what the kernels rely on between threads, the largest work lists, and
 the precision that include/tq.h states."""
+import ctypes
 import os
 import re
 import subprocess
@@ -77,6 +78,21 @@ def test_equal_shares_over_the_largest_lists(tmp_path):
     for case, (good, per) in zip(cases, out):
         assert good, case
         assert (per == 0) == (case[0] + 10 * case[1] >= 2 ** 31), case       # priced beside its units wherever that fits
+
+
+@pytest.mark.parametrize("n_q,g,n_sel,weights", [(16384, 1, 1, 0), (1, 16384, 0, 1), (16384, 1, 1 << 23, 1), (16384, 1, 0, 1),
+                                                 (8192, 2, 3, 0)])
+def test_workspaces_beyond_64_bits_are_unsupported(lib, n_q, g, n_sel, weights):
+    """Sizes that do not fit a size_t are no sizes, and the calls that would need them are refused."""
+    c = lib.tq_b8_cache(64, 1024, 65535, 64, 1 << 23, 0x10000, 0x20000, 0x30000, 0x40000)
+    r = ctypes.byref(c)
+    assert lib.lib.tq_b8_workspace_bytes(r, n_q, g, n_sel, weights) == 0
+    ws, most = 0x100000, 2 ** 64 - 1
+    if n_sel:
+        assert lib.lib.tq_b8_select(r, 0x1000, 1, n_q, g, 0, 0, n_sel, 0x2000, ws, most, None) == lib.TQ_ERR_UNSUPPORTED
+    if weights and not n_sel:
+        st = lib.lib.tq_b8_attention(r, 0x1000, 1, n_q, g, 0.1, None, 0, None, 0x5000, 1.0, 0x2000, ws, most, None)
+        assert st == lib.TQ_ERR_UNSUPPORTED
 
 
 # ----------------------------------------------------------------------------- GPU
