@@ -338,6 +338,13 @@ def _queries(cache, q):
             n_h // cache.n_kv)
 
 
+def _selection(cache, sel, n_q):
+    n_sel = sel.shape[-1] if sel.dim() else 0
+    if n_sel == 0:
+        raise ValueError(f"sel is [n_seq, n_q, n_kv, n_sel] with n_sel >= 1: got {tuple(sel.shape)}")
+    return _tensor(cache, "sel", sel, cache.i32, (cache.n_seq, n_q, cache.n_kv, n_sel)), n_sel
+
+
 def tq_b8_workspace_bytes(cache, n_q=0, g=0, n_sel=0, weights=True):
     n = lib.tq_b8_workspace_bytes(cache.ref, n_q, g, n_sel, int(weights))
     if n == 0:
@@ -380,8 +387,7 @@ def tq_b8_attention(cache, q, scale, out, ws, sel=None, acc_in=None, acc_out=Non
     op = _tensor(cache, "out", out, cache.f32, q.shape)
     sp, n_sel, ip, ap = None, 0, None, None
     if sel is not None:
-        n_sel = sel.shape[-1]
-        sp = _tensor(cache, "sel", sel, cache.i32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+        sp, n_sel = _selection(cache, sel, n_q)
     if acc_in is not None:
         ip = _tensor(cache, "acc_in", acc_in, cache.f32, cache.row)
     if acc_out is not None:
@@ -393,8 +399,7 @@ def tq_b8_attention(cache, q, scale, out, ws, sel=None, acc_in=None, acc_out=Non
 def tq_b8_select(cache, q, sel, ws, n_first=1, n_last=1, stream=None):
     """Fills sel int32 [n_seq, n_q, n_kv, n_sel] with the blocks tq_b8_attention is to look at."""
     qp, dt, n_q, g = _queries(cache, q)
-    n_sel = sel.shape[-1]
-    sp = _tensor(cache, "sel", sel, cache.i32, (cache.n_seq, n_q, cache.n_kv, n_sel))
+    sp, n_sel = _selection(cache, sel, n_q)
     return _b8_call("tq_b8_select", lib.tq_b8_select, cache, ws, stream, qp, dt, n_q, g, n_first, n_last, n_sel, sp)
 
 

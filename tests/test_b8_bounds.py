@@ -95,6 +95,21 @@ def test_workspaces_beyond_64_bits_are_unsupported(lib, n_q, g, n_sel, weights):
         assert st == lib.TQ_ERR_UNSUPPORTED
 
 
+def test_an_empty_selection_is_refused(lib):
+    """A tensor without entries has no address, which would ask for all blocks."""
+    import torch
+    d, n_kv, n_seq, nb = 64, 2, 3, 4
+    c = lib.Cache8(d, torch.zeros(12, lib.tq_b8_page_bytes(d, n_kv), dtype=torch.uint8),
+                   torch.zeros(n_seq, nb, dtype=torch.int32), torch.zeros(n_seq, dtype=torch.int32),
+                   torch.zeros(n_seq, n_kv, 2, 32, d, dtype=torch.bfloat16))
+    q, sel = torch.zeros(n_seq, 1, 4, d), torch.zeros(n_seq, 1, n_kv, 0, dtype=torch.int32)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="sel"):
+        lib.tq_b8_attention(c, q, 1.0, torch.zeros_like(q), ws, sel=sel)
+    with pytest.raises(ValueError, match="sel"):
+        lib.tq_b8_select(c, q, sel, ws, n_first=0, n_last=0)
+
+
 # ----------------------------------------------------------------------------- GPU
 @pytest.mark.gpu
 def test_selections_of_196_million_segments(m):
