@@ -147,9 +147,9 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     if (st != TQ_OK) return st;
     if ((st = check_queries(q_dtype, n_q, g)) != TQ_OK) return st;
     if (!std::isfinite(scale) || !std::isfinite(decay)) return TQ_ERR_ARG;
-    if (n_sel < 0 || (n_sel > 0) != (sel != nullptr) || n_sel > kMaxBlocks) return TQ_ERR_ARG;
+    if (n_sel < 0 || n_sel > kMaxBlocks || (c->n_seq > 0 && (n_sel > 0) != (sel != nullptr))) return TQ_ERR_ARG;
     if (acc_in && !acc_out) return TQ_ERR_ARG;
-    if (sel && acc_out && n_q != 1) return TQ_ERR_UNSUPPORTED;
+    if (n_sel && acc_out && n_q != 1) return TQ_ERR_UNSUPPORTED;
     if (c->n_seq == 0) return TQ_OK;
     if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) ||
         !aligned(acc_in, 4) || !aligned(acc_out, 4))

@@ -110,6 +110,14 @@ def test_an_empty_selection_is_refused(lib):
         lib.tq_b8_select(c, q, sel, ws, n_first=0, n_last=0)
 
 
+def test_no_sequences_with_a_selection_is_a_no_op(lib):
+    """As without one: tensors of no sequences have no addresses."""
+    r = ctypes.byref(lib.tq_b8_cache(128, 8, 0, 64, 16, 0x10000, None, None, None))
+    for n_sel in (0, 4):
+        st = lib.lib.tq_b8_attention(r, None, 1, 1, 4, 0.1, None, n_sel, None, None, 1.0, None, 0x100000, 1 << 20, None)
+        assert st == lib.TQ_OK
+
+
 # ----------------------------------------------------------------------------- GPU
 @pytest.mark.gpu
 def test_selections_of_196_million_segments(m):
