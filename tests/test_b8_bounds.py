@@ -349,3 +349,30 @@ def test_attention_queries_of_a_wide_range(m, d, g, dtype):
         within(got[s], sq, q[s], scale, lost=lost)
         within(got[s][:, :, :1], sq, q[s][:, :, :1], scale)
     assert p.ok(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g,n,where", [(128, 4, 70, 66), (64, 3, 327, 320), (128, 16, 70, 69), (256, 2, 60, 33), (80, 4, 85, 84)])
+def test_attention_sinks_in_the_open_block(m, d, g, n, where):
+    """The same where the heavy token without a value has not left the open block yet. A segment's open block comes last
+    and its weights keep 24 bits however light they are, so the full blocks' tokens keep their precision beside it."""
+    gaps = [8.0, 16.0, 20.0, 24.0, 35.0, 50.0]
+    n_kv, scale = 1, d ** -0.5
+    p = Pair(m, d, n_kv, len(gaps), n // 32 + 1, 140 + d + g, width=32768 // n_kv if g > 8 else None)
+    k = p.rng.standard_normal((len(gaps), n, n_kv, d))
+    v = p.rng.standard_normal((len(gaps), n, n_kv, d))
+    k[..., 0] = 0.0
+    k[:, n // 32 * 32:], v[:, n // 32 * 32:] = 0.0, 0.0                          # open tokens: logits of 0, no values
+    k[:, where, :, 0] = (np.array(gaps) / (4.0 * scale))[:, None]
+    fill(p, k, v)
+    q = np.rint(64 * p.rng.standard_normal((len(gaps), 1, n_kv, g, d)).clip(-3.9, 3.9)) / 64
+    q[..., 0] = 4.0
+    qt = p.torch.from_numpy(q.astype(np.float32).reshape(len(gaps), 1, n_kv * g, d)).cuda()
+    ws = p.workspace(1, g)
+    out = p.torch.full(qt.shape, float("nan"), device="cuda")
+    acc = p.torch.zeros(len(gaps), n_kv, 32 * p.nb, device="cuda")
+    m.tq_b8_attention(p.cache, qt, scale, out, ws, acc_out=acc)
+    got = out.double().cpu().numpy().reshape(q.shape)
+    for s, sq in enumerate(p.seqs):
+        within(got[s], sq, q[s], scale)
+    assert ((acc.sum(dim=-1) - g).abs() <= g * 2.0 ** -18).all() and p.ok(ws)
