@@ -118,6 +118,52 @@ def test_no_sequences_with_a_selection_is_a_no_op(lib):
         assert st == lib.TQ_OK
 
 
+def within(got, sq, q, scale, lost=0.0, n_sum=64):
+    """Output rows against 64 bits, where a logit of whole pages is off by 2^-23 of itself (its whole-number sum and its
+    distance to the block's largest in fp32), by 2^-24 max |q| max |k| (the small pieces' share of that sum) and by
+    `lost`, what q itself loses. Weights move by twice that; their pieces, exponentials, matrix products and up to n_sum
+    additions in a row are off by 2^-24 of sum w |v| each (n_sum + 64 of them in all)."""
+    want, weight, size, _ = ref.attention(sq, q, scale)
+    k = np.abs(sq.values()[:, :, 0])                                             # [n, n_kv, d]
+    logit = np.abs(scale * np.einsum("ihgd,nhd->ihgn", q, sq.values()[:, :, 0])).max(axis=-1)
+    dl = 2.0 ** -23 * logit + abs(scale) * 2.0 ** -24 * np.abs(q).max(axis=-1) * k.max() + lost
+    bound = (np.expm1(2 * dl) + (n_sum + 64) * 2.0 ** -24) * size
+    err = np.abs(got - want).max(axis=-1)
+    assert np.isfinite(got).all()
+    assert (err <= bound + 1e-30).all(), (float((err / np.maximum(bound, 1e-30)).max()), (err / np.maximum(size, 1e-300)).max(axis=(0, 1, 2)))
+    return dl
+
+
+@pytest.mark.parametrize("d,n", [(128, 64), (128, 1024), (64, 320), (256, 96)])
+def test_the_bounds_see_what_a_kernel_could_lose(d, n):
+    """Planted in the reference: weights in one fp16 piece, weights cut off 2^-20 below a heavy token without a value, and a
+    query in 14 bits are outside the bounds; fp32 weights and a query in 22 bits are inside."""
+    rng = np.random.default_rng(d + n)
+    n_kv, g, scale = 2, 4, d ** -0.5
+    sq = ref.Seq(n_kv, d)
+    k, v = rng.standard_normal((n, n_kv, d)), rng.standard_normal((n, n_kv, d))
+    k[..., 0], k[5], v[5] = 0.0, 0.0, 0.0
+    k[5, :, 0] = 16.0 / (4.0 * scale)
+    sq.append(k, v)
+    q = np.ldexp(np.rint(np.ldexp(rng.standard_normal((1, n_kv, g, d)).clip(-3.9, 3.9), 18)), -18)   # 20 bits below 4
+    q[..., 0] = 4.0
+    x = sq.values()
+
+    def answer(q, weights):
+        l = scale * np.einsum("ihgd,nhd->ihgn", q, x[:, :, 0])
+        e = np.exp(l - l.max(axis=-1, keepdims=True))
+        return np.einsum("ihgn,nhd->ihgd", weights(e), x[:, :, 1]) / e.sum(axis=-1, keepdims=True)
+
+    within(answer(q, lambda e: e.astype(np.float32).astype(np.float64)), sq, q, scale)
+    step = 4.0 * 2.0 ** -21
+    within(answer(np.rint(q / step) * step, lambda e: e), sq, q, scale)
+    for planted in (lambda: answer(q, lambda e: (e * 2.0 ** 15).astype(np.float16) / 2.0 ** 15),
+                    lambda: answer(q, lambda e: np.where(e < 2.0 ** -20, 0.0, e)),
+                    lambda: answer(np.rint(q / (step * 256)) * (step * 256), lambda e: e)):
+        with pytest.raises(AssertionError):
+            within(planted(), sq, q, scale)
+
+
 # ----------------------------------------------------------------------------- GPU
 @pytest.mark.gpu
 def test_selections_of_196_million_segments(m):
@@ -187,22 +233,6 @@ def fill(p, k, v):
     m.tq_b8_append(p.cache, cuda(k), cuda(v), p.ws)
     for s, sq in enumerate(p.seqs):
         sq.append(k[s], v[s])
-
-
-def within(got, sq, q, scale, lost=0.0, n_sum=64):
-    """Output rows against 64 bits, where a logit of whole pages is off by 2^-23 of itself (its whole-number sum and its
-    distance to the block's largest in fp32), by 2^-24 max |q| max |k| (the small pieces' share of that sum) and by
-    `lost`, what q itself loses. Weights move by twice that; their pieces, exponentials, matrix products and up to n_sum
-    additions in a row are off by 2^-24 of sum w |v| each (n_sum + 64 of them in all)."""
-    want, weight, size, _ = ref.attention(sq, q, scale)
-    k = np.abs(sq.values()[:, :, 0])                                             # [n, n_kv, d]
-    logit = np.abs(scale * np.einsum("ihgd,nhd->ihgn", q, sq.values()[:, :, 0])).max(axis=-1)
-    dl = 2.0 ** -23 * logit + abs(scale) * 2.0 ** -24 * np.abs(q).max(axis=-1) * k.max() + lost
-    bound = (np.expm1(2 * dl) + (n_sum + 64) * 2.0 ** -24) * size
-    err = np.abs(got - want).max(axis=-1)
-    assert np.isfinite(got).all()
-    assert (err <= bound + 1e-30).all(), (float((err / np.maximum(bound, 1e-30)).max()), (err / np.maximum(size, 1e-300)).max(axis=(0, 1, 2)))
-    return dl
 
 
 @pytest.mark.gpu
