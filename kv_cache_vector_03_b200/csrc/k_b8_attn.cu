@@ -49,6 +49,7 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kBias = 9.f;         // weights are kept as 2^(9 + logit - m),
 constexpr float kSlack = 6.f;        // m follows the maximum once it is passed by 2^6: 2^(9 + 6) < 65504
 constexpr float kSink = 80.f;        // tokens whose values are all zeros may pass m by 2^80
+constexpr float kMost = kBias + kSlack + kSink;
 // units a CTA takes at least, where segments are shared (one sequence of 8192 tokens: with 4 21.2 us, 8 18.6; 16 ragged ones
 // of 1500: with 8 20.5 us, 16 28.7)
 constexpr int kMinUnits = 8;
@@ -718,6 +719,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                                 float& x = sc[t >> 1][nt][2 * (t & 1) + e];
                                 const float mm = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
                                 x = __fadd_rn(__fsub_rn(__fmul_rn(x, e ? ga[nt].y : ga[nt].x), mm), kBias);
+                                if (x > kMost) x = kMost;       // (y - kSink may have been rounded to y - 128; NaN stays)
                             }
                 } else {
 #pragma unroll

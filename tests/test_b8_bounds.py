@@ -406,3 +406,47 @@ def test_attention_sinks_in_the_open_block(m, d, g, n, where):
     for s, sq in enumerate(p.seqs):
         within(got[s], sq, q[s], scale)
     assert ((acc.sum(dim=-1) - g).abs() <= g * 2.0 ** -18).all() and p.ok(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("log2_logit", [60000.0, 70000.0, 1e6, 2.0 ** 29, 1.5 * 2.0 ** 30, 1.5 * 2.0 ** 33])
+def test_weights_of_a_sink_with_a_huge_logit(m, log2_logit):
+    """A token without a value takes all of the attention, by a logit whose neighbours in fp32 lie apart: its weight is 1 a
+    row, every other one 0, and the output 0."""
+    import torch
+    d, n_kv, g, n = 64, 2, 3, 96
+    p = Pair(m, d, n_kv, 1, 4, 150)
+    k, v = p.rng.standard_normal((1, n, n_kv, d)), p.rng.standard_normal((1, n, n_kv, d))
+    k[..., 0] = 0.0
+    k[:, 40], v[:, 40] = 0.0, 0.0
+    k[:, 40, :, 0] = 64.0
+    fill(p, k, v)
+    q = torch.zeros(1, 1, n_kv * g, d, device="cuda")
+    q[..., 0], q[..., 1] = 4.0, 2.0 ** -18
+    scale = log2_logit / 256 / 1.4426950408889634
+    ws = p.workspace(1, g)
+    out, acc = torch.full(q.shape, 5.0, device="cuda"), torch.zeros(1, n_kv, 32 * p.nb, device="cuda")
+    m.tq_b8_attention(p.cache, q, scale, out, ws, acc_out=acc)
+    want = torch.zeros_like(acc)
+    want[:, :, 40] = g
+    assert ((acc - want).abs() <= g * 2.0 ** -18).all(), acc[0, :, 32:48]
+    assert torch.isfinite(out).all() and (out.abs() <= 2.0 ** -30).all() and p.ok(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.1, 1e5, -1e9])
+def test_a_seen_key_that_is_not_a_number(m, scale):
+    """A NaN in the open block's keys is every answer's that sees it, and no other's, however large the logits are."""
+    import torch
+    d, n_kv, g, n = 64, 2, 3, 70
+    p = Pair(m, d, n_kv, 2, 3, 160)
+    k, v = p.rng.standard_normal((2, n, n_kv, d)), p.rng.standard_normal((2, n, n_kv, d))
+    k[0, 67, 0, 9] = np.nan
+    fill(p, k, v)
+    q, _ = p.queries(1, g, "f32")
+    ws = p.workspace(1, g)
+    out, acc = torch.zeros(q.shape, device="cuda"), torch.zeros(2, n_kv, 32 * p.nb, device="cuda")
+    m.tq_b8_attention(p.cache, q, scale, out, ws, acc_out=acc)
+    assert torch.isnan(out[0, :, :g]).all() and torch.isnan(acc[0, 0, :n]).all()
+    assert torch.isfinite(out[0, :, g:]).all() and torch.isfinite(out[1]).all() and torch.isfinite(acc[0, 1]).all()
+    assert ((acc[1].sum(dim=-1) - g).abs() <= g * 2.0 ** -18).all() and p.ok(ws)
