@@ -383,7 +383,8 @@ int tq_b8_read(const tq_b8_cache* cache, int64_t n_tok, void* k, void* v, tq_dty
  *             as they were. acc_in (the same shape; may be acc_out itself; NULL: zeros) is read
  *             at positions below len - n_q only: newer tokens start from zero. With sel,
  *             n_q = 1 (else TQ_ERR_UNSUPPORTED) and no block may be named twice.
- *   out       device fp32 [n_seq, n_q, n_kv * g, d], 16-byte aligned.
+ *   scale     finite, and below 2^128 with log2(e).
+ *   out       device fp32 [n_seq, n_q, n_kv * g, d], 16-byte aligned, not q itself.
  *   ws        tq_b8_workspace_bytes(cache, n_q, g, n_sel, acc_out != NULL) bytes.
  * q is held in fixed point, 22 bits below a row's largest element (bf16 elements down to 2^-14 of
  * that exactly); its products with the codes are exact. A logit is off by at most

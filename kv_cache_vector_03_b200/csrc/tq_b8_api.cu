@@ -146,12 +146,13 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     int st = check_cache(c);
     if (st != TQ_OK) return st;
     if ((st = check_queries(q_dtype, n_q, g)) != TQ_OK) return st;
-    if (!std::isfinite(scale) || !std::isfinite(decay)) return TQ_ERR_ARG;
+    const double scale2 = (double)scale * 1.4426950408889634074;   // log2(e)
+    if (!std::isfinite((float)scale2) || !std::isfinite(decay)) return TQ_ERR_ARG;
     if (n_sel < 0 || n_sel > kMaxBlocks || (c->n_seq > 0 && (n_sel > 0) != (sel != nullptr))) return TQ_ERR_ARG;
     if (acc_in && !acc_out) return TQ_ERR_ARG;
     if (n_sel && acc_out && n_q != 1) return TQ_ERR_UNSUPPORTED;
     if (c->n_seq == 0) return TQ_OK;
-    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) ||
+    if (!q || !out || q == out || !aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) ||
         !aligned(acc_in, 4) || !aligned(acc_out, 4))
         return TQ_ERR_ARG;
     const B8Ws W = b8_ws(c, n_q, g, n_sel, acc_out != nullptr);
@@ -161,9 +162,8 @@ int tq_b8_attention(const tq_b8_cache* c, const void* q, tq_dtype q_dtype, int n
     std::memset(&p, 0, sizeof(p));
     p.c = view(c, ws);
     p.q = q; p.q_dtype = q_dtype; p.n_q = n_q; p.g = g;
-    const double scale2 = (double)scale * 1.4426950408889634074;   // log2(e)
     p.scale_hi = (float)scale2;
-    p.scale_lo = std::isfinite(p.scale_hi) ? (float)(scale2 - (double)p.scale_hi) : 0.f;
+    p.scale_lo = (float)(scale2 - (double)p.scale_hi);
     p.sel = sel; p.n_sel = n_sel;
     p.acc_in = acc_in; p.acc_out = acc_out; p.decay = decay;
     p.out = out;

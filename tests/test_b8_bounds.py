@@ -164,6 +164,18 @@ def test_the_bounds_see_what_a_kernel_could_lose(d, n):
             within(planted(), sq, q, scale)
 
 
+def test_attention_refuses_to_write_over_its_queries_and_scales_beyond_fp32(lib):
+    """A query row is read again by every part of its segment; scale log2(e) is held in fp32."""
+    r = ctypes.byref(lib.tq_b8_cache(128, 8, 2, 64, 16, 0x10000, 0x20000, 0x30000, 0x40000))
+
+    def call(q=0x1000, out=0x2000, scale=0.1):
+        return lib.lib.tq_b8_attention(r, q, 0, 1, 4, scale, None, 0, None, None, 1.0, out, 0x100000, 256, None)
+    assert call(out=0x1000) == lib.TQ_ERR_ARG
+    for scale in (3e38, -2.5e38):
+        assert call(scale=scale) == lib.TQ_ERR_ARG
+    assert call() == call(scale=2e38) == lib.TQ_ERR_WORKSPACE
+
+
 # ----------------------------------------------------------------------------- GPU
 @pytest.mark.gpu
 def test_selections_of_196_million_segments(m):
