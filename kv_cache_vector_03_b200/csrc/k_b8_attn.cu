@@ -31,12 +31,13 @@
 //
 // fp32 work goes two at a time (f2_*, rounded the same): 64 x 8192 181 -> 174 us.
 //
-// What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 174 us,
-// 0.94 of the measured copy rate; more in a long run at the power limit); for small ones the fixed chain launch, lengths,
-// page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of 32768: 25 us, 10 of them HBM);
-// instructions where 16 query rows share little data. A unit takes 619 warp instructions at 8 rows. The tensor pipes are
-// busy 16 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions suffice: at 8 to 16 rows a tile of 128
-// rows would be nearly empty.
+// What bounds it: HBM for large calls (64 sequences x 8192 tokens, 8 kv heads, 4 heads a group, D = 128: 1.08 GB in 177 to
+// 187 us in short runs, 0.93 to 0.88 of the measured copy rate, and 197, 0.83, in a long run at the power limit); for small
+// ones the fixed chain launch, lengths, page table, page, unit, meeting of the warps (one sequence of 500 tokens: 13 us; of
+// 32768: 25 us, 10 of them HBM); instructions where 16 query rows share little data. A unit takes 647 warp instructions at 8
+// rows. The tensor pipes are busy 16 % (fp16) and 12 % (int8) of the time, so the warp-level matrix instructions do not
+// bind. (tcgen05 could take four pages as its 128 rows and q's pieces as 24 columns: nothing gained where HBM binds, untried for
+// many query rows, where the instructions do.)
 #include <algorithm>
 #include <cfloat>
 
@@ -122,8 +123,8 @@ TQ_DEVICE uint32_t atomic_add_acq_rel(uint32_t* at, uint32_t v) {
 }
 
 // ------------------------------------------------------------------------ the list of units
-// "virtual sequences": a sequence, or with a selection one query token of it. The host has checked that
-// all units together, and the units of one virtual sequence over all heads and tiles, count below 2^30.
+// "virtual sequences": a sequence, or with a selection one query token of it. The host has checked that (blocks + 1) x
+// segments is at most 2^30; a segment has at most two units more than blocks, so there are at most 3 * 2^29 units.
 template <bool SP>
 TQ_DEVICE int virt_units(const B8AttnParams& p, int v, int& n) {
     const int s = SP && p.n_q > 1 ? v / p.n_q : v;
@@ -1256,7 +1257,7 @@ int b8_attn_grid() { return std::min(kCtasPerSm * tq_device_sms(), 2 * kB8Counte
 
 cudaError_t b8_launch_attention(const B8AttnParams& p, cudaStream_t st) {
     const int64_t virt = p.sel ? p.c.n_seq * p.n_q : p.c.n_seq;
-    // the kernel counts units in 31 bits
+    // the kernel counts units in 31 bits (and their price, b8_shares.h)
     const int64_t most = (p.sel ? p.n_sel : p.c.max_blocks) + 1;
     if (virt * p.c.n_kv * p.row_tiles > 0x3fffffffLL || most * (virt * p.c.n_kv * p.row_tiles) > 0x3fffffffLL)
         return cudaErrorInvalidValue;
