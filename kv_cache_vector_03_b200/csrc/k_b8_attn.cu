@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::warps * 32, kCtasPerSm) k_b8_att
                     big = __any_sync(0xffffffffu, big);
                 }
                 if (big) {
-                    // Beyond 2^16 m itself is rounded by more than a weight could show: subtract the rounded logits,
-                    // of which the largest is m exactly.
+                    // Beyond 2^16 exact logits pass the rounded ones, from which m comes, by more than a weight could show: take
+                    // the rounded ones.
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
